@@ -23,6 +23,10 @@
  *   C   the fresh-context variant of the cache (context K/V recomputed at the step that
  *       uses them, not reused from the block's last evaluation): dp_context_refresh,
  *       dp_context_refresh_sublayer
+ *   D   projections in microscaled 4-bit floating point: dp_mx4_quantize,
+ *       dp_mx4_dequantize, dp_mx4_linear
+ *   E   attention over packed sequences of different lengths, grouped heads, causal or not
+ *       (prompts, chunks behind a prefix, single tokens over a cache): dp_packed_attention
  *
  * Conventions (all entry points):
  *  - Token tensors are row-major [rows][hidden], hidden = n_heads * head_dim, channel
@@ -448,6 +452,82 @@ dp_status dp_context_refresh(const void* k_ctx, const void* v_ctx, int64_t n_ctx
 dp_status dp_context_refresh_sublayer(const void* x_ctx, int64_t n_ctx, const dp_blocks* ctx_blk,
                                       const void* w_qkv, const float* b_qkv, float eps,
                                       dp_kvcache* cache, void* work, void* stream);
+
+/* ---------------------------------------------------------------- D: 4-bit projections */
+
+/*
+ * Microscaled 4-bit floating point (the OCP Microscaling Formats specification v1.0, FP4):
+ * a matrix [rows][k], k a multiple of 32, is held as
+ *   codes   DEVICE [rows][k / 2] bytes: element 2 i of a row in the low half of its byte i,
+ *           2 i + 1 in the high half; each the sign and the magnitude 0, 0.5, 1, 1.5, 2, 3,
+ *           4 or 6 (e2m1);
+ *   scales  DEVICE bytes, one for each 32 elements of a row: s stands for 2^(s - 127), 255
+ *           for NaN.  They lie in tiles of 128 rows by 4 blocks (512 bytes, the order in
+ *           which the tensor cores read them): with t = ceil(k / 128), block b of row r is
+ *           byte ((r / 128) * t + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.
+ *           dp_mx4_scale_bytes gives the size; the bytes that stand for no block are 0.
+ */
+#define DP_MX4_BLOCK 32
+
+/* Bytes of the scales of [rows][k]: ceil(rows / 128) * ceil(k / 128) * 512.  INVALID_ARG for
+ * rows < 0, k <= 0 or k no multiple of 32. */
+dp_status dp_mx4_scale_bytes(int64_t rows, int32_t k, int64_t* bytes);
+
+/* Quantise x (DEVICE [n_rows][k], bf16, f16 or f32): for each block of 32, with m its largest
+ * magnitude, e = max(floor(log2 m) - 2, -127), s = e + 127, and each element x / 2^e (exact)
+ * rounded to the nearest code, ties to the even one, saturating at 6.  A block of zeros gets
+ * s = 0; one that holds an infinity or a NaN gets s = 255, and all of it then reads as NaN.
+ * Every byte of codes and of the scales (those of no block too) is written.  n_rows = 0 does
+ * nothing. */
+dp_status dp_mx4_quantize(const void* x, int64_t n_rows, int32_t k, dp_dtype x_dt, void* codes, void* scales,
+                          void* stream);
+
+/* The values that codes and scales stand for: y DEVICE [n_rows][k], bf16 or f32 (exact; what
+ * underflows in y's type is rounded) or f16 (rounded to nearest even, saturating at +-65504). */
+dp_status dp_mx4_dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y, dp_dtype y_dt,
+                            void* stream);
+
+/* y = a W^T + bias with both operands in 4 bits: a [m][k] and w [n][k] as codes and scales
+ * (w's rows are the out-features), bias DEVICE [n] float or NULL, y DEVICE [m][n] of y_dt
+ * (bf16, f16 saturating at +-65504, or f32).  The products are exact, their sums fp32, rounded
+ * once to y's type.  n a multiple of 8, k of 32 (UNSUPPORTED otherwise).  m = 0 does nothing.
+ * y overlaps no input. */
+dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, const void* w_scales, const float* bias,
+                        int64_t m, int32_t n, int32_t k, void* y, dp_dtype y_dt, void* stream);
+
+/* ---------------------------------------------------------------- E: packed attention */
+
+#define DP_MAX_SEQS 1024  /* sequences of one dp_packed_attention */
+
+/* dp_packed_attention flags */
+#define DP_CAUSAL 1u
+
+/* Attention over n_seqs sequences packed one behind the other (q_lens, k_lens, k_starts: HOST
+ * arrays).  Sequence i owns q_lens[i] query rows (behind those of the sequences before it) and
+ * the key rows [k_starts[i], k_starts[i] + k_lens[i]); k_starts = NULL: one behind the other
+ * like the queries.  Key ranges may overlap (a shared prefix) and leave rows out (a padded
+ * cache).  Its queries are the sequence's last rows: with DP_CAUSAL query t sees the keys
+ * j <= k_lens[i] - q_lens[i] + t, without it all k_lens[i].
+ *   out_t,h = sum_j softmax_j(q_t,h . k_j,g * softmax_scale) v_j,g,   g = h / (n_heads / n_kv_heads)
+ *   lse_t,h = log sum_j exp(q_t,h . k_j,g * softmax_scale)
+ * A query that sees no key (k_lens[i] = 0, or causal with more queries than keys) gets out = 0
+ * and lse = -infinity.
+ * q, out: DEVICE [q_rows][n_heads][head_dim], k, v: DEVICE [k_rows][n_kv_heads][head_dim], all
+ * of dt, rows ld_* elements apart (so that they may be column ranges of one buffer; multiples
+ * of 16 bytes); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
+ * sequence are neither read nor written, key rows of no sequence affect nothing, whatever they
+ * hold.  The rows of a sequence have to be finite: a value that the causal mask hides takes
+ * part in a product with weight 0.
+ * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32)
+ * or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
+ * <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative length or start, n_seqs outside
+ * [1, DP_MAX_SEQS], sequences that reach behind q_rows or k_rows, and an out or lse whose
+ * address range overlaps another tensor's.  No query rows: nothing is done. */
+dp_status dp_packed_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                              void* out, int64_t ld_out, float* lse, int64_t q_rows, int64_t k_rows,
+                              const int64_t* q_lens, const int64_t* k_lens, const int64_t* k_starts, int32_t n_seqs,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float softmax_scale,
+                              uint32_t flags, dp_dtype dt, void* stream);
 
 /* ---------------------------------------------------------------- profiling */
 

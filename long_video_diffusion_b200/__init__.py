@@ -12,6 +12,8 @@ The calls mirror include/dp.h:
                                         and gate (+ residual) epilogue
   kvcache_advance, queue_push/pop   A3  queue and cache advance
   window_step                       A4  the whole step
+  mx4_quantize/dequantize/linear    D   projections in microscaled 4-bit floating point
+  packed_attention                  E   attention over packed sequences, grouped heads
 """
 from __future__ import annotations
 
@@ -33,6 +35,9 @@ MOD_Q, GATE_OUT = 1, 2
 TEST_SKIP_KV_LOADS = 0x80000000
 STEP_POP = 1
 STEP_CACHE_ALL_SLOTS = 2
+CAUSAL = 1
+MAX_SEQS = 1024
+MX4_BLOCK = 32
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python long_video_diffusion_b200/_build.py` "
@@ -108,6 +113,12 @@ _SIGS = {
     "dp_context_refresh": [_P, _P, _I64, ctypes.POINTER(DpBlocks), ctypes.POINTER(DpKvcache), _I32, _P],
     "dp_context_refresh_sublayer": [_P, _I64, ctypes.POINTER(DpBlocks), _P, _P, _F, ctypes.POINTER(DpKvcache), _P,
                                     _P],
+    "dp_mx4_scale_bytes": [_I64, _I32, ctypes.POINTER(_I64)],
+    "dp_mx4_quantize": [_P, _I64, _I32, _I32, _P, _P, _P],
+    "dp_mx4_dequantize": [_P, _P, _I64, _I32, _P, _I32, _P],
+    "dp_mx4_linear": [_P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _I32, _P],
+    "dp_packed_attention": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, ctypes.POINTER(_I64),
+                            ctypes.POINTER(_I64), ctypes.POINTER(_I64), _I32, _I32, _I32, _I32, _F, _U32, _I32, _P],
     "dp_profile_begin": [_I32],
     "dp_profile_end": [ctypes.POINTER(_F), ctypes.POINTER(_F), ctypes.POINTER(_F), ctypes.POINTER(_I32)],
     "dp_profile_end_stages": [ctypes.POINTER(_F), _I32, ctypes.POINTER(_I32), ctypes.POINTER(_I32)],
@@ -529,6 +540,134 @@ def sublayer_planes(work, n_win: int, hidden: int):
     k = work[2 * plane:3 * plane].view(torch.float16).view(n_win, hidden)
     v = work[3 * plane:4 * plane].view(torch.float16).view(n_win, hidden)
     return o, q, k, v
+
+
+# ------------------------------------------------------------------------- D: 4-bit projections
+
+def _same_device(ref: torch.Tensor, *others) -> int:
+    """The CUDA device index of ref; the other tensors (None left out) have to be there too."""
+    if not ref.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    dev = ref.get_device()
+    for t in others:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("tensors on different devices")
+    return dev
+
+
+def _call(fn, where: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with device `dev` current, on `stream` or dev's current stream."""
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != OK:
+        raise DpError(st, where)
+
+
+def mx4_scale_bytes(rows: int, k: int) -> int:
+    """Bytes of the scales of a [rows][k] matrix in 4 bits (dp_mx4_scale_bytes)."""
+    out = _I64()
+    _check(_lib.dp_mx4_scale_bytes(int(rows), int(k), ctypes.byref(out)), "dp_mx4_scale_bytes")
+    return out.value
+
+
+def mx4_empty(rows: int, k: int, device=None):
+    """(codes, scales): uninitialised buffers for a [rows][k] matrix in 4 bits."""
+    dev = device or "cuda"
+    return (torch.empty(rows, k // 2, dtype=torch.uint8, device=dev),
+            torch.empty(mx4_scale_bytes(rows, k), dtype=torch.uint8, device=dev))
+
+
+def _mx4(codes: torch.Tensor, scales: torch.Tensor, what: str):
+    """(rows, k) of a 4-bit matrix, its buffers checked."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2:
+        raise ValueError(f"{what}: codes must be uint8 [rows, k / 2] and scales uint8")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    rows, k = codes.shape[0], 2 * codes.shape[1]
+    if scales.numel() < -(-rows // 128) * -(-k // 128) * 512:
+        raise ValueError(f"{what}: scales hold fewer than mx4_scale_bytes({rows}, {k}) bytes")
+    return rows, k
+
+
+def mx4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """x [rows][k] (bf16, f16 or f32) to microscaled 4-bit codes and scales (dp_mx4_quantize);
+    codes uint8 [rows][k / 2], scales uint8 of at least mx4_scale_bytes(rows, k)."""
+    dev = _same_device(x, codes, scales)
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [rows, k]")
+    if _mx4(codes, scales, "mx4_quantize") != tuple(x.shape):
+        raise ValueError("codes must be [rows, k / 2] for x [rows, k]")
+    _call(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, x.data_ptr(), x.shape[0], x.shape[1], _dtype(x),
+          codes.data_ptr(), scales.data_ptr())
+
+
+def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """The values that codes and scales stand for (dp_mx4_dequantize); y [rows][k] bf16, f16 or f32."""
+    dev = _same_device(y, codes, scales)
+    if y.dim() != 2 or not y.is_contiguous():
+        raise ValueError("y must be a contiguous [rows, k]")
+    if _mx4(codes, scales, "mx4_dequantize") != tuple(y.shape):
+        raise ValueError("y must be [rows, k] for codes [rows, k / 2]")
+    _call(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), y.shape[0],
+          y.shape[1], y.data_ptr(), _dtype(y))
+
+
+def mx4_linear(a, a_scales, w, w_scales, bias, y, stream=None) -> None:
+    """y = a W^T + bias on 4-bit operands (dp_mx4_linear): a [m][k] and w [n][k] as codes and
+    scales, bias float [n] or None, y [m][n] bf16, f16 or f32."""
+    dev = _same_device(y, a, a_scales, w, w_scales, bias)
+    m, k = _mx4(a, a_scales, "a")
+    n, kw = _mx4(w, w_scales, "w")
+    if kw != k or y.shape != (m, n) or not y.is_contiguous():
+        raise ValueError(f"a [{m}, {k}], w [{n}, {kw}] and a contiguous y {tuple(y.shape)} do not match")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n,) or not bias.is_contiguous()):
+        raise ValueError("bias must be float32 [n]")
+    _call(_lib.dp_mx4_linear, "dp_mx4_linear", dev, stream, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
+          w_scales.data_ptr(), None if bias is None else bias.data_ptr(), m, n, k, y.data_ptr(), _dtype(y))
+
+
+# ------------------------------------------------------------------------- E: packed attention
+
+def _pitch(t: torch.Tensor, what: str) -> int:
+    """Elements between rows of t [rows, heads, head_dim], whose rows must be contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [rows, heads, head_dim]")
+    rows, heads, d = t.shape
+    if (t.stride(2) != 1 and d > 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: a row's heads must be contiguous")
+    return t.stride(0) if rows > 1 else heads * d
+
+
+def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
+                     k_starts: Optional[Sequence[int]] = None, causal: bool = True, lse=None,
+                     softmax_scale: float = 0.0, stream=None) -> None:
+    """Attention over packed sequences of different lengths (dp_packed_attention).  q, out
+    [q_rows, heads, head_dim] and k, v [k_rows, kv_heads, head_dim], bf16, f16 or f32, rows at
+    any pitch (column ranges of one buffer will do); sequence i owns q_lens[i] query rows, one
+    behind the other, and the key rows [k_starts[i], k_starts[i] + k_lens[i]) (k_starts=None: one
+    behind the other too).  Its queries are its last rows: causal, query t sees the keys
+    j <= k_lens[i] - q_lens[i] + t.  lse: float32 [q_rows, heads] or None.  A query that sees no
+    key gets out = 0 and lse = -inf; rows behind the last sequence are left as they are."""
+    dev = _same_device(q, k, v, out, lse)
+    n = len(q_lens)
+    if len(k_lens) != n or (k_starts is not None and len(k_starts) != n):
+        raise ValueError("q_lens, k_lens and k_starts differ in length")
+    lq, lk, lv, lo = _pitch(q, "q"), _pitch(k, "k"), _pitch(v, "v"), _pitch(out, "out")
+    if out.shape != q.shape or k.shape != v.shape or q.shape[2] != k.shape[2]:
+        raise ValueError("shapes of q and out, or of k and v, or their head_dim differ")
+    if k.dtype != q.dtype or v.dtype != q.dtype or out.dtype != q.dtype:
+        raise TypeError("q, k, v and out differ in dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [q_rows, heads]")
+    arr = _I64 * n
+    _call(_lib.dp_packed_attention, "dp_packed_attention", dev, stream, q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
+          lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(), q.shape[0], k.shape[0], arr(*q_lens),
+          arr(*k_lens), None if k_starts is None else arr(*k_starts), n, q.shape[1], k.shape[1], q.shape[2],
+          softmax_scale, CAUSAL if causal else 0, _dtype(q))
 
 
 def profile_begin(max_steps: int) -> None:

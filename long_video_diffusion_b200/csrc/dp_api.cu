@@ -980,6 +980,185 @@ dp_status dp_sublayer_step(const void* x, int64_t n_win, const dp_blocks* blk, c
   return DP_OK;
 }
 
+// ------------------------------------------------------------------ D: 4-bit projections
+
+namespace {
+
+dp_status check_mx4(int64_t rows, int32_t k) {
+  if (rows < 0 || rows > INT32_MAX) return fail(DP_ERR_INVALID_ARG, "rows %lld", static_cast<long long>(rows));
+  if (k <= 0) return fail(DP_ERR_INVALID_ARG, "k %d", k);
+  if (k % DP_MX4_BLOCK) return fail(DP_ERR_UNSUPPORTED, "k %d (a multiple of %d)", k, DP_MX4_BLOCK);
+  return DP_OK;
+}
+
+int64_t mx4_scale_size(int64_t rows, int32_t k) { return (rows + 127) / 128 * ((static_cast<int64_t>(k) + 127) / 128) * 512; }
+
+}  // namespace
+
+dp_status dp_mx4_scale_bytes(int64_t rows, int32_t k, int64_t* bytes) {
+  if (!bytes) return fail(DP_ERR_INVALID_ARG, "bytes is NULL");
+  if (rows < 0 || rows > INT32_MAX || k <= 0 || k % DP_MX4_BLOCK)
+    return fail(DP_ERR_INVALID_ARG, "rows %lld, k %d (a positive multiple of %d)", static_cast<long long>(rows), k,
+                DP_MX4_BLOCK);
+  *bytes = mx4_scale_size(rows, k);
+  return DP_OK;
+}
+
+dp_status dp_mx4_quantize(const void* x, int64_t n_rows, int32_t k, dp_dtype x_dt, void* codes, void* scales,
+                          void* stream) {
+  if (!dtype_ok(x_dt)) return fail(DP_ERR_INVALID_ARG, "dtype");
+  dp_status st = check_mx4(n_rows, k);
+  if (st != DP_OK) return st;
+  if (n_rows == 0) return DP_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(DP_ERR_INVALID_ARG, "x/codes/scales NULL or misaligned");
+  const int64_t xb = n_rows * k * elem_bytes(x_dt), cb = n_rows * k / 2, sb = mx4_scale_size(n_rows, k);
+  if (overlaps(x, xb, codes, cb) || overlaps(x, xb, scales, sb) || overlaps(codes, cb, scales, sb))
+    return fail(DP_ERR_INVALID_ARG, "x, codes and scales must not overlap");
+  cudaError_t e = dp::launch_mx4_quantize(x, n_rows, k, x_dt, codes, scales, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 quantize launch");
+  return DP_OK;
+}
+
+dp_status dp_mx4_dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y, dp_dtype y_dt,
+                            void* stream) {
+  if (!dtype_ok(y_dt)) return fail(DP_ERR_INVALID_ARG, "dtype");
+  dp_status st = check_mx4(n_rows, k);
+  if (st != DP_OK) return st;
+  if (n_rows == 0) return DP_OK;
+  if (!y || !codes || !scales || !aligned16(y) || !aligned16(codes) || !aligned16(scales))
+    return fail(DP_ERR_INVALID_ARG, "codes/scales/y NULL or misaligned");
+  const int64_t yb = n_rows * k * elem_bytes(y_dt);
+  if (overlaps(y, yb, codes, n_rows * k / 2) || overlaps(y, yb, scales, mx4_scale_size(n_rows, k)))
+    return fail(DP_ERR_INVALID_ARG, "y overlaps an input");
+  cudaError_t e = dp::launch_mx4_dequantize(codes, scales, n_rows, k, y, y_dt, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 dequantize launch");
+  return DP_OK;
+}
+
+dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, const void* w_scales, const float* bias,
+                        int64_t m, int32_t n, int32_t k, void* y, dp_dtype y_dt, void* stream) {
+  if (!dtype_ok(y_dt)) return fail(DP_ERR_INVALID_ARG, "dtype");
+  dp_status st = check_mx4(m, k);
+  if (st != DP_OK) return st;
+  if (n <= 0) return fail(DP_ERR_INVALID_ARG, "n %d", n);
+  if (n % 8) return fail(DP_ERR_UNSUPPORTED, "n %d (a multiple of 8)", n);
+  if (m == 0) return DP_OK;
+  if (!a || !a_scales || !w || !w_scales || !y) return fail(DP_ERR_INVALID_ARG, "a/w/scales/y NULL");
+  if (!aligned16(a) || !aligned16(a_scales) || !aligned16(w) || !aligned16(w_scales) || !aligned16(y) ||
+      (bias && !aligned16(bias)))
+    return fail(DP_ERR_INVALID_ARG, "pointer not 16-byte aligned");
+  const int64_t yb = m * n * elem_bytes(y_dt);
+  if (overlaps(y, yb, a, m * k / 2) || overlaps(y, yb, a_scales, mx4_scale_size(m, k)) ||
+      overlaps(y, yb, w, static_cast<int64_t>(n) * k / 2) || overlaps(y, yb, w_scales, mx4_scale_size(n, k)) ||
+      (bias && overlaps(y, yb, bias, static_cast<int64_t>(n) * 4)))
+    return fail(DP_ERR_INVALID_ARG, "y overlaps an input");
+  dp::Mx4Args g;
+  g.a = a;
+  g.a_scales = a_scales;
+  g.w = w;
+  g.w_scales = w_scales;
+  g.bias = bias;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.y = y;
+  g.y_dt = y_dt;
+  st = status_ptr(&g.status);
+  if (st != DP_OK) return st;
+  cudaError_t e = dp::launch_mx4_linear(g, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 linear launch");
+  return DP_OK;
+}
+
+// ------------------------------------------------------------------ E: packed attention
+
+dp_status dp_packed_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                              void* out, int64_t ld_out, float* lse, int64_t q_rows, int64_t k_rows,
+                              const int64_t* q_lens, const int64_t* k_lens, const int64_t* k_starts, int32_t n_seqs,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float softmax_scale,
+                              uint32_t flags, dp_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return fail(DP_ERR_INVALID_ARG, "dtype");
+  if (flags & ~DP_CAUSAL) return fail(DP_ERR_INVALID_ARG, "flags 0x%x", flags);
+  if (n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_heads % n_kv_heads)
+    return fail(DP_ERR_INVALID_ARG, "n_heads %d, n_kv_heads %d", n_heads, n_kv_heads);
+  if (head_dim != 64 && head_dim != 128) return fail(DP_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", head_dim);
+  if (n_heads > 32767) return fail(DP_ERR_UNSUPPORTED, "n_heads %d (at most 32767)", n_heads);
+  if (std::isnan(softmax_scale) || std::isinf(softmax_scale)) return fail(DP_ERR_INVALID_ARG, "softmax_scale");
+  if (!q_lens || !k_lens) return fail(DP_ERR_INVALID_ARG, "q_lens/k_lens NULL");
+  if (n_seqs < 1 || n_seqs > DP_MAX_SEQS) return fail(DP_ERR_INVALID_ARG, "n_seqs %d outside [1, %d]", n_seqs, DP_MAX_SEQS);
+  if (q_rows < 0 || q_rows > INT32_MAX || k_rows < 0 || k_rows > INT32_MAX)
+    return fail(DP_ERR_INVALID_ARG, "q_rows/k_rows outside [0, 2^31)");
+  int32_t first_q[DP_MAX_SEQS], q_len[DP_MAX_SEQS], first_k[DP_MAX_SEQS], k_len[DP_MAX_SEQS];
+  int32_t n = 0;
+  int64_t nq = 0, nk = 0;
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    const int64_t start = k_starts ? k_starts[i] : nk;
+    if (q_lens[i] < 0 || q_lens[i] > q_rows - nq)
+      return fail(DP_ERR_INVALID_ARG, "q_lens[%d] = %lld reaches behind the %lld query rows", i,
+                  static_cast<long long>(q_lens[i]), static_cast<long long>(q_rows));
+    if (k_lens[i] < 0 || start < 0 || start > k_rows || k_lens[i] > k_rows - start)
+      return fail(DP_ERR_INVALID_ARG, "keys of sequence %d (start %lld, length %lld) reach outside the %lld key rows", i,
+                  static_cast<long long>(start), static_cast<long long>(k_lens[i]), static_cast<long long>(k_rows));
+    if (q_lens[i] > 0) {
+      first_q[n] = static_cast<int32_t>(nq);
+      q_len[n] = static_cast<int32_t>(q_lens[i]);
+      first_k[n] = static_cast<int32_t>(start);
+      k_len[n] = static_cast<int32_t>(k_lens[i]);
+      n += 1;
+    }
+    nq += q_lens[i];
+    nk += k_lens[i];
+  }
+  const int64_t eb = elem_bytes(dt);
+  const int64_t wq = static_cast<int64_t>(n_heads) * head_dim, wk = static_cast<int64_t>(n_kv_heads) * head_dim;
+  const int64_t most_ld = int64_t(1) << 31;
+  if (ld_q < wq || ld_out < wq || ld_k < wk || ld_v < wk || ld_q > most_ld || ld_out > most_ld || ld_k > most_ld || ld_v > most_ld)
+    return fail(DP_ERR_INVALID_ARG, "row pitches %lld %lld %lld %lld", static_cast<long long>(ld_q),
+                static_cast<long long>(ld_k), static_cast<long long>(ld_v), static_cast<long long>(ld_out));
+  if ((ld_q * eb) % 16 || (ld_k * eb) % 16 || (ld_v * eb) % 16 || (ld_out * eb) % 16)
+    return fail(DP_ERR_INVALID_ARG, "row pitch not a multiple of 16 bytes");
+  if (n == 0) return DP_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || (lse && !aligned16(lse)))
+    return fail(DP_ERR_INVALID_ARG, "q/out/lse NULL or misaligned");
+  if (k_rows > 0 && (!k || !v || !aligned16(k) || !aligned16(v)))
+    return fail(DP_ERR_INVALID_ARG, "k/v NULL or misaligned");
+  const int64_t qb = ((q_rows - 1) * ld_q + wq) * eb, ob = ((q_rows - 1) * ld_out + wq) * eb;
+  const int64_t kb = k_rows ? ((k_rows - 1) * ld_k + wk) * eb : 0, vb = k_rows ? ((k_rows - 1) * ld_v + wk) * eb : 0;
+  const int64_t lb = lse ? q_rows * n_heads * 4 : 0;
+  if (overlaps(out, ob, q, qb) || (kb && overlaps(out, ob, k, kb)) || (vb && overlaps(out, ob, v, vb)))
+    return fail(DP_ERR_INVALID_ARG, "out overlaps an input");
+  if (lse && (overlaps(lse, lb, out, ob) || overlaps(lse, lb, q, qb) || (kb && overlaps(lse, lb, k, kb)) ||
+              (vb && overlaps(lse, lb, v, vb))))
+    return fail(DP_ERR_INVALID_ARG, "lse overlaps another tensor");
+  dp::PackedArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.ld_q = ld_q;
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.ld_out = ld_out;
+  a.n_seqs = n;
+  a.first_q = first_q;
+  a.q_len = q_len;
+  a.first_k = first_k;
+  a.k_len = k_len;
+  a.n_heads = n_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.head_dim = head_dim;
+  a.softmax_scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+  a.causal = (flags & DP_CAUSAL) != 0;
+  a.dt = dt;
+  dp_status st = status_ptr(&a.status);
+  if (st != DP_OK) return st;
+  cudaError_t e = dp::launch_packed(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "packed attention launch");
+  return DP_OK;
+}
+
 // ------------------------------------------------------------------ the queue's schedule (host)
 
 namespace {

@@ -138,6 +138,55 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s);
 cudaError_t launch_ln_modulate(const void* x, void* h, int64_t n_rows, int hidden, float eps, const BlockTable& bt,
                                cudaStream_t s);
 
+// Microscaled 4-bit rows (dp_mx4.cu).  Scale byte of block b of row r; tiles = ceil(k / 128).
+__host__ __device__ __forceinline__ int64_t mx4_scale_at(int64_t r, int32_t b, int32_t tiles) {
+  return ((r >> 7) * tiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+cudaError_t launch_mx4_quantize(const void* x, int64_t n_rows, int32_t k, dp_dtype x_dt, void* codes, void* scales,
+                                cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y,
+                                  dp_dtype y_dt, cudaStream_t s);
+
+// y = a W^T + bias on 4-bit operands (dp_mx4_gemm.cu).
+struct Mx4Args {
+  const void* a;
+  const void* a_scales;
+  const void* w;
+  const void* w_scales;
+  const float* bias;  // [n] or NULL
+  int64_t m;
+  int32_t n;          // multiple of 8
+  int32_t k;          // multiple of 32
+  void* y;            // [m][n]
+  dp_dtype y_dt;
+  uint32_t* status;
+};
+cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s);
+
+// Attention over packed sequences (dp_packed_f32.cu, dp_packed_tc.cu).  Only sequences with query rows;
+// first_q[i] is sequence i's first query row.
+struct PackedArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;  // or NULL
+  int64_t ld_q, ld_k, ld_v, ld_out;  // elements
+  int32_t n_seqs;
+  const int32_t* first_q;
+  const int32_t* q_len;
+  const int32_t* first_k;
+  const int32_t* k_len;
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  float softmax_scale;
+  bool causal;
+  dp_dtype dt;
+  uint32_t* status;
+};
+cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s);
+
 // Host-side helper: encode a 2-D 16-bit (f16 or bf16) tensor map [rows][hidden] with a
 // {64 columns, box_rows rows} box and 128-byte swizzle (defined in dp_attn_tc.cu).
 bool encode_tmap_16(void* tmap, const void* base, int64_t rows, int hidden, int box_rows, bool f16);

@@ -1,0 +1,225 @@
+// Attention over packed sequences of different lengths, grouped heads, causal or not, on the
+// CUDA cores: every sum in fp32.
+//
+//   out_t,h = sum_j softmax_j(q_t,h . k_j,g * scale) v_j,g,  g = h / group,
+//   j < k_len, causal j <= k_len - q_len + t;  lse_t,h = log sum_j exp(q_t,h . k_j,g * scale)
+//
+// One pass over the keys with a running maximum and sum.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+
+#include "dp_device.cuh"
+#include "dp_packed.h"
+
+namespace dp {
+
+int64_t plan_packed(const PackedArgs& a, int rows, int32_t* n, int32_t* tile0, int32_t* first_q, int32_t* q_len,
+                    int32_t* first_k, int32_t* k_len) {
+  int32_t order[DP_MAX_SEQS];
+  for (int i = 0; i < a.n_seqs; ++i) order[i] = i;
+  std::sort(order, order + a.n_seqs, [&](int32_t x, int32_t y) {
+    return a.k_len[x] != a.k_len[y] ? a.k_len[x] > a.k_len[y] : x < y;
+  });
+  const int64_t group = a.n_heads / a.n_kv_heads;
+  int64_t tiles = 0;
+  *n = a.n_seqs;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int32_t o = order[i];
+    tile0[i] = static_cast<int32_t>(tiles);
+    first_q[i] = a.first_q[o];
+    q_len[i] = a.q_len[o];
+    first_k[i] = a.first_k[o];
+    k_len[i] = a.k_len[o];
+    if (a.q_len[o] * group > INT_MAX) return -1;
+    tiles += (a.q_len[o] * group + rows - 1) / rows;
+    if (tiles > INT_MAX) return -1;
+  }
+  tile0[a.n_seqs] = static_cast<int32_t>(tiles);
+  return tiles;
+}
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kRowsPerWarp = 8;
+constexpr int kRows = kWarps * kRowsPerWarp;  // query rows per block
+constexpr int kKeys = 32;                     // keys per tile: one per lane
+
+struct Strides {
+  int64_t q, k, v, out;
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const T* h = reinterpret_cast<const T*>(&x);
+    return make_float4(static_cast<float>(h[0]), static_cast<float>(h[1]), static_cast<float>(h[2]), static_cast<float>(h[3]));
+  }
+}
+
+// A warp's eight rows against one tile of 32 keys: lane j holds key j's scores, then each lane
+// its columns of the output.
+template <typename T, int HD, int N>
+__global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                                  const T* __restrict__ v, T* __restrict__ out,
+                                                                  float* __restrict__ lse, Strides ld,
+                                                                  const __grid_constant__ PackedSeqs<N> seqs,
+                                                                  int n_heads, int group, float scale, int causal) {
+  extern __shared__ float smem[];
+  constexpr int KP = HD + 4;  // pitch of a key row: 16-byte reads of 32 rows without conflicts
+  float* sk = smem;           // [kKeys][KP]
+  float* sv = sk + kKeys * KP;  // [kKeys][HD]
+  float* sq = sv + kKeys * HD;  // [kRows][HD], scaled
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x, kv = blockIdx.y;
+  const int s = seq_of_tile(seqs, tile);
+  const int q_len = seqs.q_len[s], k_len = seqs.k_len[s];
+  const int rows = q_len * group;
+  const int row0 = (seqs.tile0[s + 1] - 1 - tile) * kRows;
+  const int n_rows = min(kRows, rows - row0);
+  const int seen = min(k_len, keys_seen((row0 + n_rows - 1) / group, q_len, k_len, causal));  // by the tile's last row
+
+  for (int i = threadIdx.x; i < kRows * (HD / 4); i += 32 * kWarps) {
+    const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+    float4 x = make_float4(0, 0, 0, 0);
+    if (r < n_rows) {
+      const int tok = (row0 + r) / group, h = kv * group + (row0 + r) % group;
+      x = load4(q + (seqs.first_q[s] + static_cast<int64_t>(tok)) * ld.q + h * HD + c);
+    }
+    float* d = sq + r * HD + c;
+    d[0] = x.x * scale, d[1] = x.y * scale, d[2] = x.z * scale, d[3] = x.w * scale;
+  }
+  int lim[kRowsPerWarp];
+  float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][HD / 32];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const int row = row0 + warp * kRowsPerWarp + r;
+    lim[r] = row < rows ? min(k_len, keys_seen(row / group, q_len, k_len, causal)) : 0;
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) acc[r][c] = 0.0f;
+  }
+  for (int j0 = 0; j0 < seen; j0 += kKeys) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kKeys * (HD / 4); i += 32 * kWarps) {
+      const int j = i / (HD / 4), c = (i % (HD / 4)) * 4;
+      float4 x = make_float4(0, 0, 0, 0), y = x;
+      if (j0 + j < k_len) {
+        const int64_t row = seqs.first_k[s] + static_cast<int64_t>(j0 + j);
+        x = load4(k + row * ld.k + kv * HD + c);
+        y = load4(v + row * ld.v + kv * HD + c);
+      }
+      *reinterpret_cast<float4*>(sk + j * KP + c) = x;
+      *reinterpret_cast<float4*>(sv + j * HD + c) = y;
+    }
+    __syncthreads();
+    if (warp * kRowsPerWarp >= n_rows) continue;
+    float dot[kRowsPerWarp] = {};
+    const float* kr = sk + lane * KP;
+    const float* qr = sq + warp * kRowsPerWarp * HD;
+#pragma unroll 4
+    for (int c = 0; c < HD; c += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(kr + c);
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) {
+        const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
+        dot[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r]))));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r) {
+      const float x = j0 + lane < lim[r] ? dot[r] : -INFINITY;
+      float t = x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      const float mn = fmaxf(m[r], t);
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      const float f = expf(m[r] - ref);
+      const float p = expf(x - ref);
+      m[r] = mn;
+      float sum = p;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l[r] = l[r] * f + sum;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) acc[r][c] *= f;
+      dot[r] = p;
+    }
+    const int n_keys = min(kKeys, seen - j0);
+    for (int j = 0; j < n_keys; ++j) {
+      float y[HD / 32];
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) y[c] = sv[j * HD + c * 32 + lane];
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) {
+        const float p = __shfl_sync(0xffffffffu, dot[r], j);
+        if (j0 + j < lim[r]) {  // uniform in the warp: what the mask hides is not multiplied
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) acc[r][c] = fmaf(p, y[c], acc[r][c]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) {
+    const int row = row0 + warp * kRowsPerWarp + r;
+    if (row >= rows) break;
+    const int64_t tok = seqs.first_q[s] + static_cast<int64_t>(row / group);
+    const int h = kv * group + row % group;
+    const float inv = lim[r] > 0 ? 1.0f / l[r] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c)
+      out[tok * ld.out + h * HD + c * 32 + lane] = static_cast<T>(lim[r] > 0 ? acc[r][c] * inv : 0.0f);
+    if (lse && lane == 0) lse[tok * n_heads + h] = lim[r] > 0 ? m[r] + logf(l[r]) : -INFINITY;
+  }
+}
+
+template <typename T, int HD, int N>
+cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
+  PackedSeqs<N> s;
+  const int64_t tiles = plan_packed(a, kRows, s);
+  if (tiles < 0 || a.n_kv_heads > 65535) return cudaErrorInvalidValue;
+  constexpr int bytes = (kKeys * (HD + 4) + kKeys * HD + kRows * HD) * 4;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> attr_set[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(packed_simt_kernel<T, HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  packed_simt_kernel<T, HD, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
+      static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), static_cast<T*>(a.out), a.lse,
+      Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, a.n_heads, a.n_heads / a.n_kv_heads, a.softmax_scale, a.causal);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const PackedArgs& a, cudaStream_t st) {
+  if (a.n_seqs <= kFewSeqs)
+    return a.head_dim == 64 ? launch_n<T, 64, kFewSeqs>(a, st) : launch_n<T, 128, kFewSeqs>(a, st);
+  return a.head_dim == 64 ? launch_n<T, 64, DP_MAX_SEQS>(a, st) : launch_n<T, 128, DP_MAX_SEQS>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s) {
+  if (a.n_seqs < 1 || a.n_seqs > DP_MAX_SEQS || (a.head_dim != 64 && a.head_dim != 128)) return cudaErrorInvalidValue;
+  if (a.dt == DP_F32) return launch_t<float>(a, s);
+  if (a.dt == DP_BF16) return launch_t<__nv_bfloat16>(a, s);
+  return launch_t<__half>(a, s);
+}
+
+}  // namespace dp

@@ -44,6 +44,11 @@ Parity status of each function (how it is pinned, in tests/test_oracle_pins.py):
                     pinned: a hand-worked selection; first window = the pool in order;
                     later blocks distinct, disjoint from the previous block, in permutation
                     order; gathered rows equal the pool's frames
+  mx4_quantize / mx4_values / mx4_scale_index
+                    pinned: hand-worked blocks (ties, saturation, zeros, denormals, NaN);
+                    every code a nearest one; the scale tiles a permutation
+  packed_attention  pinned: brute-force loops; window_attention's special case; hand-worked
+                    masks; empty rows
 """
 from .dualparal import (as_f64, row_blocks, lookup, modulate, modulate_rounded,
                         window_attention, window_step, KVCacheRing, FifoQueue,
@@ -51,10 +56,13 @@ from .dualparal import (as_f64, row_blocks, lookup, modulate, modulate_rounded,
 from .sublayer import round_to, layer_norm, ln_modulate, linear, sublayer_step
 from .noise_init import coordinated_frames, coordinated_schedule, gather_frames
 from .context import fresh_context, fresh_context_sublayer
+from .mx4 import mx4_quantize, mx4_values, mx4_scale_index
+from .packed import packed_attention
 
 __all__ = ["as_f64", "row_blocks", "lookup", "modulate", "modulate_rounded",
            "window_attention", "window_step", "KVCacheRing", "FifoQueue", "entry_step",
            "long_run_schedule", "timestep_schedule", "LongRun", "round_to", "layer_norm",
            "ln_modulate", "linear", "sublayer_step", "coordinated_frames",
            "coordinated_schedule", "gather_frames", "fresh_context",
-           "fresh_context_sublayer"]
+           "fresh_context_sublayer", "mx4_quantize", "mx4_values", "mx4_scale_index",
+           "packed_attention"]
