@@ -751,10 +751,14 @@ cudaError_t launch_hd(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 bool encode_tmap_16(void* tmap, const void* base, int64_t rows, int hidden, int box_rows, bool f16) {
+  return encode_tmap_16_pitch(tmap, base, rows, hidden, hidden, box_rows, f16);
+}
+
+bool encode_tmap_16_pitch(void* tmap, const void* base, int64_t rows, int hidden, int64_t pitch, int box_rows, bool f16) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(hidden), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(hidden) * 2};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
   cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(static_cast<CUtensorMap*>(tmap), f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,

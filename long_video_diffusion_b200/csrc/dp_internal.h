@@ -186,9 +186,12 @@ struct PackedArgs {
   uint32_t* status;
 };
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s);
+cudaError_t launch_packed_tc(const PackedArgs& a, cudaStream_t s);  // bf16, f16
 
 // Host-side helper: encode a 2-D 16-bit (f16 or bf16) tensor map [rows][hidden] with a
 // {64 columns, box_rows rows} box and 128-byte swizzle (defined in dp_attn_tc.cu).
 bool encode_tmap_16(void* tmap, const void* base, int64_t rows, int hidden, int box_rows, bool f16);
+// The same with rows `pitch` elements apart.
+bool encode_tmap_16_pitch(void* tmap, const void* base, int64_t rows, int hidden, int64_t pitch, int box_rows, bool f16);
 
 }  // namespace dp

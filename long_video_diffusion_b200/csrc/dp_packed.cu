@@ -218,8 +218,7 @@ cudaError_t launch_t(const PackedArgs& a, cudaStream_t st) {
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s) {
   if (a.n_seqs < 1 || a.n_seqs > DP_MAX_SEQS || (a.head_dim != 64 && a.head_dim != 128)) return cudaErrorInvalidValue;
   if (a.dt == DP_F32) return launch_t<float>(a, s);
-  if (a.dt == DP_BF16) return launch_t<__nv_bfloat16>(a, s);
-  return launch_t<__half>(a, s);
+  return launch_packed_tc(a, s);
 }
 
 }  // namespace dp

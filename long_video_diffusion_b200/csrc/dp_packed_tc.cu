@@ -1,0 +1,722 @@
+// Attention over packed sequences on the sm_100a tensor cores (bf16 or f16; the fp32 form is in
+// dp_packed.cu, which also states the formulas).
+//
+// One block = one k/v head's two tiles of 128 query rows of one sequence; a row is a (token,
+// head of the group) pair (dp_packed.h), so that a tile's keys are read once for all the heads
+// that share them and a single token fills as many rows as its group has heads.  Keys go by in
+// tiles of BN rows (128 at head_dim 64, 64 at head_dim 128) up to the last one that a row of the
+// tile sees; only tiles that the mask cuts pay for it (warp-uniform test).
+//   warps 0-3  softmax of query tile 0, one thread per row
+//   warps 4-7  softmax of query tile 1
+//   warp 8     TMA producer: K and V tiles into a ring of shared-memory stages
+//   warps 9-11 issue S_g = Q_g K^T and O_g += P_g V, the same number of products each
+//              (head_dim 64: S of both tiles, PV_0, PV_1; head_dim 128: S_0, S_1, PV of both)
+// Tensor memory holds S (fp32), P (16 bits, the A operand of PV) and O of both tiles.  The
+// softmax runs in fp32 in units of log2 with a running maximum that O is rescaled for only when
+// it grows by more than 2^8; P is rounded to the operands' 16-bit type (the tensor cores take
+// nothing wider beside 16-bit V), the row sum takes it unrounded.
+//
+// Few rows and many keys (single tokens over a cache): the keys are cut into as many parts as a
+// thread-block cluster has blocks, each block keeps its part's O, maximum and sum, and at the
+// end the blocks join them through distributed shared memory, in a fixed order, with no
+// workspace and no second launch.
+//
+// A tile of keys that ends behind its sequence holds other rows: their scores are masked, and
+// the producer warp writes zeros over their V rows before the product reads them (0 * NaN).
+// Every wait is bounded (dp_device.cuh).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cmath>
+
+#include "dp_device.cuh"
+#include "dp_packed.h"
+
+namespace dp {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int NQ = 2;            // query tiles per block
+constexpr int kTileRows = NQ * BM;
+constexpr int kTmemCols = 512;
+constexpr int kMaxSplits = 8;    // portable cluster size
+constexpr float kRescaleLog2 = 8.0f;
+
+// 2^x on the FMA pipe for some columns (the MUFU unit gives 16 exponentials per clock and SM, as
+// many as the tensor cores need at head_dim 128): n = round(x), 2^n p(x - n), p the degree-4
+// minimax polynomial of 2^f on [-1/2, 1/2] (csrc/fit_exp2_poly.py with DEGREE = 4; relative error
+// 2.7e-6, so that the row sum and the log-sum-exp keep fp32's use).
+constexpr float kC0 = 0.9999992847442627f, kC1 = 0.6931217908859253f, kC2 = 0.240247443318367f;
+constexpr float kC3 = 0.05591785907745361f, kC4 = 0.009570102207362652f;
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+constexpr float kMinX = -125.0f;
+constexpr uint32_t kPolyMask = 0x1111u;  // column pairs of each 16 that use it
+
+template <int HD>
+struct Lay {
+  static constexpr int BN = HD == 64 ? 128 : 64;
+  static constexpr int W_PROD = 4 * NQ;
+  static constexpr int W_ISS = W_PROD + 1;
+  static constexpr int kThreads = 32 * (W_PROD + 4);
+  static constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
+  static constexpr int kLowRegs = 72, kHighRegs = 216;
+  static_assert(NQ * 128 * kHighRegs + 128 * kLowRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
+  static constexpr int KCH = HD / 64;
+  static constexpr int STAGES = 4;
+  static constexpr int Q_CHUNK = BM * 128;
+  static constexpr int KV_CHUNK = BN * 128;
+  static constexpr int Q_BYTES = BM * HD * 2;
+  static constexpr int KV_BYTES = BN * HD * 2;
+  static constexpr bool S_PER_TILE = HD > BN;  // the issuers' split (see above)
+  static constexpr int COL_S = HD >= BN ? NQ * HD : 0;
+  static constexpr int COL_P = COL_S + NQ * BN;
+  static constexpr int COL_O = HD >= BN ? 0 : COL_P + NQ * (BN / 2);
+  static_assert(NQ * (BN + BN / 2 + HD) <= kTmemCols, "tensor memory budget");
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = NQ * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
+  static constexpr int N_BAR = 3 * STAGES + 5 * NQ + 2;
+  static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int ALLOC = BYTES + 1024;
+  // a split's result for the join, over Q, K and V: O rows (a pitch that spreads the banks),
+  // then (maximum, sum) per row
+  static constexpr int O_PITCH = HD + 4;
+  static constexpr int OFF_ML = kTileRows * O_PITCH * 4;
+  static_assert(OFF_ML + kTileRows * 8 <= OFF_BAR, "the join's rows fit before the barriers");
+  static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+struct PackedParams {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  int64_t ld_q, ld_out;
+  int32_t n_heads, n_kv, group;
+  int32_t splits;  // blocks per cluster
+  int32_t causal;
+  float scale_log2;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Shared address `a` of this block in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float2 ld_peer2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+template <int HD, bool F16, int N>
+__global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
+    packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const PackedParams p, const __grid_constant__ PackedSeqs<N> seqs) {
+  using L = Lay<HD>;
+  constexpr int BN = L::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // this block's rows and its part of their keys
+  const int rank = blockIdx.x % p.splits;
+  const int item = blockIdx.x / p.splits;
+  const int kv = item % p.n_kv;
+  const int tile = item / p.n_kv;
+  const int seq = seq_of_tile(seqs, tile);
+  const int q_len = seqs.q_len[seq], k_len = seqs.k_len[seq];
+  const int first_q = seqs.first_q[seq], first_k = seqs.first_k[seq];
+  const int rows = q_len * p.group;
+  const int row0 = (seqs.tile0[seq + 1] - 1 - tile) * kTileRows;
+  int nt[NQ];  // key tiles of each query tile, then those of this block's part
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) {
+    const int end = min(rows, row0 + (g + 1) * BM);  // behind the query tile's last row
+    const int seen = end > row0 + g * BM ? min(k_len, keys_seen((end - 1) / p.group, q_len, k_len, p.causal)) : 0;
+    nt[g] = (seen + BN - 1) / BN;
+  }
+  const int per = (max(nt[0], nt[1]) + p.splits - 1) / p.splits;
+  const int t_begin = rank * per;
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) nt[g] = max(0, min(nt[g] - t_begin, per));
+  const int n_loc = max(nt[0], nt[1]);
+  // the last tile of the part ends behind the sequence
+  const int tail_rows = n_loc > 0 ? k_len - (t_begin + n_loc - 1) * BN : BN;
+  const bool tail = tail_rows < BN;
+
+  const uint32_t bar0 = sb + L::OFF_BAR;
+  auto k_full = [&](int s) { return bar0 + 8u * s; };
+  auto v_full = [&](int s) { return bar0 + 8u * (L::STAGES + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (2 * L::STAGES + s); };
+  auto q_full = [&](int g) { return bar0 + 8u * (3 * L::STAGES + g); };
+  auto s_full = [&](int g) { return bar0 + 8u * (3 * L::STAGES + NQ + g); };
+  auto s_free = [&](int g) { return bar0 + 8u * (3 * L::STAGES + 2 * NQ + g); };
+  auto p_full = [&](int g) { return bar0 + 8u * (3 * L::STAGES + 3 * NQ + g); };
+  auto o_done = [&](int g) { return bar0 + 8u * (3 * L::STAGES + 4 * NQ + g); };
+  const uint32_t fin = bar0 + 8u * (3 * L::STAGES + 5 * NQ);
+  const uint32_t v_fixed = fin + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::STAGES; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(kv_empty(s), L::S_PER_TILE ? 1 : NQ);
+    }
+    for (int g = 0; g < NQ; ++g) {
+      mbar_init(q_full(g), 128);
+      mbar_init(s_full(g), 1);
+      mbar_init(s_free(g), 128);
+      mbar_init(p_full(g), 128);
+      mbar_init(o_done(g), 1);
+    }
+    mbar_init(fin, 3);
+    mbar_init(v_fixed, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == L::W_ISS) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == L::W_PROD && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= L::W_PROD) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLowRegs));
+    if (warp == L::W_PROD) {
+      // ------------------------------------------------------------ TMA producer
+      int issued = 0;
+      if (lane == 0) {
+        for (int j = 0; j < n_loc; ++j) {
+          const int st = j % L::STAGES;
+          const int use = j / L::STAGES;
+          if (use > 0 && !mbar_wait(kv_empty(st), (use - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
+          const int row = first_k + (t_begin + j) * BN;
+          mbar_arrive_expect_tx(k_full(st), L::KV_BYTES);
+#pragma unroll
+          for (int c = 0; c < L::KCH; ++c)
+            tma_load_2d(sb + L::OFF_K + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_k, kv * HD + c * 64, row, k_full(st));
+          mbar_arrive_expect_tx(v_full(st), L::KV_BYTES);
+#pragma unroll
+          for (int c = 0; c < L::KCH; ++c)
+            tma_load_2d(sb + L::OFF_V + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_v, kv * HD + c * 64, row, v_full(st));
+          issued = j + 1;
+        }
+      }
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      if (tail && issued == n_loc) {
+        const int j = n_loc - 1, st = j % L::STAGES;
+        bool ok = mbar_wait(v_full(st), (j / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV);
+        if (__all_sync(0xffffffffu, ok)) {
+          for (int i = tail_rows * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+            for (int c = 0; c < L::KCH; ++c)
+              *reinterpret_cast<uint4*>(smem + L::OFF_V + st * L::KV_BYTES + c * L::KV_CHUNK + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_fixed);
+        }
+      }
+      if (lane == 0) {
+        // every copy this block issued lands before its shared memory is released
+        const int first = issued > L::STAGES ? issued - L::STAGES : 0;
+        for (int j = first; j < issued; ++j) {
+          mbar_drain_wait(k_full(j % L::STAGES), (j / L::STAGES) & 1, p.status);
+          mbar_drain_wait(v_full(j % L::STAGES), (j / L::STAGES) & 1, p.status);
+        }
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuers
+      constexpr uint32_t idS = idesc_f32acc(Operand<F16>::kFmt, BM, BN, false);
+      constexpr uint32_t idPV = idesc_f32acc(Operand<F16>::kFmt, BM, HD, true);
+      auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
+        return mbar_wait(bar, parity, abort, p.status, code);
+      };
+      const uint64_t dq0 = sdesc_sw128(sb + L::OFF_Q, 16, 1024);
+      const uint64_t dk0 = sdesc_sw128(sb + L::OFF_K, 16, 1024);
+      const uint64_t dv0 = sdesc_sw128(sb + L::OFF_V, L::KV_CHUNK, 1024);
+      bool ok = wait(q_full(0), 0, DEV_ERR_TIMEOUT_Q) && wait(q_full(1), 0, DEV_ERR_TIMEOUT_Q);
+      // S_g of tile t, once K_t is there and S_g of tile t - 1 is in the softmax's registers
+      auto do_s = [&](int t, int g) {
+        const int st = t % L::STAGES;
+        ok = (t == 0 || wait(s_free(g), (t - 1) & 1, DEV_ERR_TIMEOUT_S)) &&
+             wait(k_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dq = dq0 + static_cast<uint64_t>((g * L::Q_BYTES) >> 4);
+        const uint64_t dk = dk0 + static_cast<uint64_t>((st * L::KV_BYTES) >> 4);
+        const uint32_t d = tmem + L::COL_S + g * BN;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t oq = static_cast<uint64_t>(((kk >> 2) * L::Q_CHUNK + (kk & 3) * 32) >> 4);
+          const uint64_t ok_ = static_cast<uint64_t>(((kk >> 2) * L::KV_CHUNK + (kk & 3) * 32) >> 4);
+          mma_ss(d, dq + oq, dk + ok_, idS, kk > 0);
+        }
+        mma_commit(s_full(g));
+      };
+      // O_g += P_g V of tile t
+      auto do_pv = [&](int t, int g) {
+        const int st = t % L::STAGES;
+        ok = wait(p_full(g), t & 1, DEV_ERR_TIMEOUT_P) && wait(v_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV) &&
+             (!tail || t != n_loc - 1 || wait(v_fixed, 0, DEV_ERR_TIMEOUT_KV));
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dv = dv0 + static_cast<uint64_t>((st * L::KV_BYTES) >> 4);
+        const uint32_t pa = tmem + L::COL_P + g * (BN / 2);
+        const uint32_t d = tmem + L::COL_O + g * HD;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(d, pa + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idPV, (t > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(o_done(g));
+      };
+      const int iw = warp - L::W_ISS;
+      if constexpr (L::S_PER_TILE) {
+        if (iw < NQ) {
+          const int n = iw == 0 ? nt[0] : nt[1];
+          for (int t = 0; ok && t < n; ++t) do_s(t, iw);
+        } else {
+          for (int t = 0; ok && t < n_loc; ++t) {
+            if (t < nt[0]) do_pv(t, 0);
+            if (ok && t < nt[1]) do_pv(t, 1);
+            if (ok) mma_commit(kv_empty(t % L::STAGES));
+          }
+        }
+      } else {
+        if (iw == 0) {
+          for (int t = 0; ok && t < n_loc; ++t) {
+            if (t < nt[0]) do_s(t, 0);
+            if (ok && t < nt[1]) do_s(t, 1);
+          }
+        } else {
+          const int g = iw - 1;
+          const int n = g == 0 ? nt[0] : nt[1];
+          for (int t = 0; ok && t < n_loc; ++t) {
+            const int st = t % L::STAGES;
+            if (t < n) {
+              do_pv(t, g);
+              if (ok) mma_commit(kv_empty(st));
+            } else {
+              // not this query tile's: its arrival for the stage, once per fill
+              ok = wait(v_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV);
+              if (ok) mbar_arrive(kv_empty(st));
+            }
+          }
+        }
+      }
+      // every product this warp issued completes before tensor memory is released
+      mma_commit(fin);
+      mbar_drain_wait(fin, 0, p.status);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kHighRegs));
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2;
+    const int t = threadIdx.x & 127;
+    const int my_nt = g == 0 ? nt[0] : nt[1];
+    const int row = row0 + g * BM + t;
+    const bool row_ok = row < rows;
+    const int tok = row_ok ? row / p.group : 0;
+    const int head = kv * p.group + (row_ok ? row - tok * p.group : 0);
+    // keys that this row sees (a row behind the last one needs no mask: nothing of it is stored)
+    const int lim = row_ok ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : INT_MAX;
+
+    {
+      uint8_t* sq = smem + L::OFF_Q + g * L::Q_BYTES;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (first_q + static_cast<int64_t>(tok)) * p.ld_q + head * HD);
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sq + (c >> 3) * L::Q_CHUNK + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full(g));
+    }
+
+    const uint32_t trow = tmem + ((static_cast<uint32_t>(warp & 3) * 32u) << 16);
+    const uint32_t s_col = trow + L::COL_S + g * BN;
+    const uint32_t p_col = trow + L::COL_P + g * (BN / 2);
+    const uint32_t o_col = trow + L::COL_O + g * HD;
+    constexpr int NCH = BN / 32;
+    constexpr int NG = BN / 16;
+    const uint64_t sl2 = f32x2(p.scale_log2, p.scale_log2);
+    const bool live = __any_sync(0xffffffffu, row_ok);
+    // tiles of this part that every row of the warp sees whole
+    const int n_whole = __reduce_min_sync(0xffffffffu, lim) / BN - t_begin;
+    float m_ref = -INFINITY;
+    float l_sum = 0.0f;
+    bool ok = true;
+
+    for (int j = 0; j < my_nt; ++j) {
+      ok = mbar_wait(s_full(g), j & 1, abort, p.status, DEV_ERR_TIMEOUT_S);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (!live) {  // no rows: keep the barriers going, P's no sooner than the others may
+        mbar_arrive(s_free(g));
+        if (j > 0) {
+          ok = mbar_wait(o_done(g), (j - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        mbar_arrive(p_full(g));
+        continue;
+      }
+      tc_fence_after();
+      uint32_t sr[NCH][32];
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) tmem_ld32(s_col + i * 32, sr[i]);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(s_free(g));
+      const bool cut = j >= n_whole;
+      const int valid = lim - (t_begin + j) * BN;  // columns of this tile that the row sees
+      if (cut) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (i * 32 + c >= valid) sr[i][c] = 0xff800000u;
+      }
+      float mc[NG];
+#pragma unroll
+      for (int h = 0; h < NG; ++h) {
+        const uint32_t* r = &sr[h >> 1][(h & 1) * 16];
+        float m = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[15]));
+#pragma unroll
+        for (int c = 1; c < 15; c += 2) m = fmax3(m, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        mc[h] = m;
+      }
+      float mx;
+      if constexpr (NG == 8)
+        mx = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+      else
+        mx = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
+      const float m_new = fmaxf(m_ref, mx * p.scale_log2);
+      if (j == 0) {
+        m_ref = m_new;
+      } else {
+        const bool need = m_new > m_ref + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          ok = mbar_wait(o_done(g), (j - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = need ? ex2_approx(m_ref - m_new) : 1.0f;
+#pragma unroll
+          for (int c0 = 0; c0 < HD; c0 += 32) {
+            uint32_t orr[32];
+            tmem_ld32(o_col + c0, orr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
+            tmem_st32(o_col + c0, orr);
+          }
+          tmem_wait_st();
+          if (need) {
+            l_sum *= f;
+            m_ref = m_new;
+          }
+        }
+      }
+      // a row that has seen no key yet has no maximum: all its scores are -inf, all its weights 0
+      const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
+      const uint64_t nm2 = f32x2(-ref, -ref);
+      const uint64_t magic2 = f32x2(kMagic, kMagic), nmagic2 = f32x2(-kMagic, -kMagic), neg1_2 = f32x2(-1.0f, -1.0f);
+      const uint64_t c0_2 = f32x2(kC0, kC0), c1_2 = f32x2(kC1, kC1), c2_2 = f32x2(kC2, kC2);
+      const uint64_t c3_2 = f32x2(kC3, kC3), c4_2 = f32x2(kC4, kC4);
+      uint64_t acc0 = f32x2(0.0f, 0.0f), acc1 = acc0;
+      uint32_t pk[NCH][16];
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint64_t x = ffma2(f32x2(__uint_as_float(sr[i][2 * c]), __uint_as_float(sr[i][2 * c + 1])), sl2, nm2);
+          float x0, x1, a, b;
+          f32x2_split(x, x0, x1);
+          if ((kPolyMask >> c) & 1u) {
+            const uint64_t xc = f32x2(fmaxf(x0, kMinX), fmaxf(x1, kMinX));
+            const uint64_t r = fadd2(xc, magic2);
+            const uint64_t f = ffma2(fadd2(r, nmagic2), neg1_2, xc);
+            uint64_t q = ffma2(c4_2, f, c3_2);
+            q = ffma2(q, f, c2_2);
+            q = ffma2(q, f, c1_2);
+            q = ffma2(q, f, c0_2);
+            float q0, q1, r0, r1;
+            f32x2_split(q, q0, q1);
+            f32x2_split(r, r0, r1);
+            a = __int_as_float(__float_as_int(q0) + (__float_as_int(r0) << 23));
+            b = __int_as_float(__float_as_int(q1) + (__float_as_int(r1) << 23));
+          } else {
+            a = ex2_approx(x0);
+            b = ex2_approx(x1);
+          }
+          const uint64_t ab = f32x2(a, b);
+          if (c & 1)
+            acc1 = fadd2(acc1, ab);
+          else
+            acc0 = fadd2(acc0, ab);
+          pk[i][c] = pack2<F16>(a, b);
+        }
+      }
+      if (cut) {
+        // the polynomial gives 2^-125, not 0, for a masked column: nothing in the sum, but no
+        // weight may be left on the V rows behind it
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if ((kPolyMask >> c) & 1u) {
+              if (i * 32 + 2 * c >= valid) pk[i][c] &= 0xffff0000u;
+              if (i * 32 + 2 * c + 1 >= valid) pk[i][c] &= 0xffffu;
+            }
+      }
+      if (j > 0) {
+        // P of tile j - 1 has been read
+        ok = mbar_wait(o_done(g), (j - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) tmem_st16(p_col + i * 16, pk[i]);
+      float a0, a1;
+      f32x2_split(fadd2(acc0, acc1), a0, a1);
+      l_sum += a0 + a1;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full(g));
+    }
+
+    if (ok && my_nt > 0) {
+      ok = mbar_wait(o_done(g), (my_nt - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const bool sees = lim > 0;
+    if (p.splits == 1) {
+      if (ok && live) {
+        const float inv_l = 1.0f / l_sum;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + (first_q + static_cast<int64_t>(tok)) * p.ld_out + head * HD);
+#pragma unroll
+        for (int c0 = 0; c0 < HD; c0 += 32) {
+          uint32_t r[32];
+          if (my_nt > 0) {
+            tmem_ld32(o_col + c0, r);
+            tmem_wait_ld();
+          }
+          if (row_ok) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<F16>(__uint_as_float(r[c * 8 + 2 * e]) * inv_l, __uint_as_float(r[c * 8 + 2 * e + 1]) * inv_l);
+              dst[c0 / 8 + c] = sees ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        if (p.lse && row_ok)
+          p.lse[(first_q + static_cast<int64_t>(tok)) * p.n_heads + head] =
+              sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+      }
+    } else {
+      // the part's result where the join finds it; Q, K and V have been read once both
+      // warpgroups are here
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (ok && live) {
+        float* od = reinterpret_cast<float*>(smem) + (g * BM + t) * L::O_PITCH;
+        if (my_nt > 0) {
+#pragma unroll
+          for (int c0 = 0; c0 < HD; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_col + c0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<uint4*>(od + c0 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+          }
+        }
+        // a part in which the row saw nothing: weight 0, its O (unwritten, or a product of zeros) unread
+        reinterpret_cast<float2*>(smem + L::OFF_ML)[g * BM + t] = make_float2(my_nt > 0 ? m_ref : -INFINITY, l_sum);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::W_ISS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (p.splits > 1) {
+    cluster_sync();
+    // block `rank` joins the rows r = rank, rank + splits, ...: four columns per thread
+    const int n_rows = min(kTileRows, rows - row0);
+    const int n_mine = (n_rows - rank + p.splits - 1) / p.splits;
+    for (int i = threadIdx.x; i < n_mine * (HD / 4); i += L::kThreads) {
+      const int r = rank + (i / (HD / 4)) * p.splits;
+      const int c = (i % (HD / 4)) * 4;
+      float2 ml[kMaxSplits];
+      float4 o[kMaxSplits];
+      float top = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < kMaxSplits; ++s)
+        if (s < p.splits) {
+          ml[s] = ld_peer2(peer_smem(sb + L::OFF_ML + r * 8, s));
+          o[s] = ld_peer4(peer_smem(sb + (r * L::O_PITCH + c) * 4, s));
+          top = fmaxf(top, ml[s].x);
+        }
+      float4 a = make_float4(0, 0, 0, 0);
+      float l = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kMaxSplits; ++s)
+        if (s < p.splits && ml[s].x != -INFINITY) {
+          const float w = ex2_approx(ml[s].x - top);
+          l = fmaf(w, ml[s].y, l);
+          a.x = fmaf(w, o[s].x, a.x);
+          a.y = fmaf(w, o[s].y, a.y);
+          a.z = fmaf(w, o[s].z, a.z);
+          a.w = fmaf(w, o[s].w, a.w);
+        }
+      const int row = row0 + r;
+      const int tok = row / p.group;
+      const int head = kv * p.group + row - tok * p.group;
+      const bool sees = top != -INFINITY;
+      const float inv = sees ? 1.0f / l : 0.0f;
+      const int64_t at = first_q + static_cast<int64_t>(tok);
+      *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
+          make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+      if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+    cluster_sync();  // no block leaves while another reads its shared memory
+  }
+}
+
+// Blocks per cluster: one, unless the block with the most key tiles would run longer than an even
+// share of all tiles over the SMs; each part keeps at least four tiles, about the cost of a
+// block's start and join.
+int choose_splits(const PackedArgs& a, int bn, int sms) {
+  const int group = a.n_heads / a.n_kv_heads;
+  int64_t most = 0, total = 0;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int64_t row_tiles = (static_cast<int64_t>(a.q_len[i]) * group + kTileRows - 1) / kTileRows;
+    const int64_t key_tiles = (static_cast<int64_t>(a.k_len[i]) + bn - 1) / bn;
+    most = key_tiles > most ? key_tiles : most;
+    total += row_tiles * key_tiles * a.n_kv_heads;
+  }
+  int splits = 1;
+  while (splits < kMaxSplits && most > 4 * 2 * splits - 1 && most * sms > total * splits) splits *= 2;
+  return splits;
+}
+
+template <int HD, bool F16, int N>
+cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
+  using L = Lay<HD>;
+  PackedSeqs<N> seqs;
+  const int64_t tiles = plan_packed(a, kTileRows, seqs);
+  int64_t key_rows = 0;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int64_t end = static_cast<int64_t>(a.first_k[i]) + a.k_len[i];
+    if (a.k_len[i] > 0 && end > key_rows) key_rows = end;
+  }
+  CUtensorMap tk, tv;
+  // with no keys at all nothing is loaded: any rows will do for the maps
+  const void* k = key_rows ? a.k : a.q;
+  const void* v = key_rows ? a.v : a.q;
+  const int cols = a.n_kv_heads * HD;
+  if (!encode_tmap_16_pitch(&tk, k, key_rows ? key_rows : 1, cols, key_rows ? a.ld_k : a.ld_q, L::BN, F16) ||
+      !encode_tmap_16_pitch(&tv, v, key_rows ? key_rows : 1, cols, key_rows ? a.ld_v : a.ld_q, L::BN, F16))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  auto kernel = packed_attn_tc_kernel<HD, F16, N>;
+  static std::atomic<bool> attr_set[64];
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;  // setmaxnreg.inc would wait for good
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  PackedParams p;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.ld_q = a.ld_q;
+  p.ld_out = a.ld_out;
+  p.n_heads = a.n_heads;
+  p.n_kv = a.n_kv_heads;
+  p.group = a.n_heads / a.n_kv_heads;
+  p.splits = choose_splits(a, L::BN, sms);
+  p.causal = a.causal;
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.status = a.status;
+  const int64_t grid = tiles * a.n_kv_heads * p.splits;
+  if (tiles < 0 || grid > INT_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::ALLOC;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p, seqs);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int HD, bool F16>
+cudaError_t launch_hd(const PackedArgs& a, cudaStream_t s) {
+  return a.n_seqs <= kFewSeqs ? launch_n<HD, F16, kFewSeqs>(a, s) : launch_n<HD, F16, DP_MAX_SEQS>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_tc(const PackedArgs& a, cudaStream_t s) {
+  if (a.head_dim == 64) return a.dt == DP_F16 ? launch_hd<64, true>(a, s) : launch_hd<64, false>(a, s);
+  return a.dt == DP_F16 ? launch_hd<128, true>(a, s) : launch_hd<128, false>(a, s);
+}
+
+}  // namespace dp
