@@ -750,6 +750,8 @@ cudaError_t launch_hd(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode_fn(); }
+
 bool encode_tmap_16(void* tmap, const void* base, int64_t rows, int hidden, int box_rows, bool f16) {
   return encode_tmap_16_pitch(tmap, base, rows, hidden, hidden, box_rows, f16);
 }

@@ -2,7 +2,9 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <vector_types.h>
 
 #include "dp.h"
@@ -187,6 +189,9 @@ struct PackedArgs {
 };
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s);
 cudaError_t launch_packed_tc(const PackedArgs& a, cudaStream_t s);  // bf16, f16
+
+// The driver's tensor-map encoder, NULL if it has none (defined in dp_attn_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Host-side helper: encode a 2-D 16-bit (f16 or bf16) tensor map [rows][hidden] with a
 // {64 columns, box_rows rows} box and 128-byte swizzle (defined in dp_attn_tc.cu).

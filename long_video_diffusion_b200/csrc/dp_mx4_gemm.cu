@@ -1,7 +1,24 @@
-// y = a W^T + bias with both operands in microscaled 4-bit floating point.
+// y = a W^T + bias with both operands in microscaled 4-bit floating point, on the sm_100a tensor
+// cores: tcgen05.mma kind::mxf4 takes the e2m1 codes from shared memory (packed, two to a byte,
+// 256 of a row in one 128-byte swizzle row) and one power-of-two scale per 32 of them from
+// tensor memory, and sums exact products in fp32.
+//
+// A step is 256 of k: TMA brings the codes' tiles and the scales' (whose layout in memory, tiles
+// of 128 rows by 128 columns in 512 bytes, is the one tcgen05.cp spreads over tensor memory);
+// what lies behind k or behind the last row arrives as zeros.  Scales alternate between two
+// column ranges of tensor memory, so that a step's copy never meets the step before's products.
+//
+// Few rows of a (mx4_narrow_kernel): bound by reading W once.  W's rows are the tile's M (128
+// features per block), the tokens its N, and k is cut into as many parts as a cluster has blocks,
+// so that all SMs read W at once; the parts are summed through distributed shared memory in a
+// fixed order.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <climits>
 
 #include "dp_device.cuh"
 #include "dp_internal.h"
@@ -10,61 +27,345 @@ namespace dp {
 
 namespace {
 
-constexpr int kTile = 64;
+constexpr int kStepK = 256;        // of k per step: 128 bytes of codes
+constexpr int kScaleTile = 512;    // bytes: 128 rows x 128 of k
+constexpr int kMaxSplits = 8;      // portable cluster size
 
-__device__ __forceinline__ float mx4_value(const uint8_t* codes, const uint8_t* scales, int64_t row, int col, int k, int tiles) {
-  const uint32_t v = codes[(row * k + col) >> 1] >> (4 * (col & 1));
-  const uint32_t s = scales[mx4_scale_at(row, col >> 5, tiles)], mag = v & 7u;
-  const float scale = s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s ? s << 23 : 0x00400000u);
-  const float a = mag < 2u ? 0.5f * static_cast<float>(mag) : __uint_as_float(((126u + (mag >> 1)) << 23) | ((mag & 1u) << 22));
-  return ((v & 8u) ? -a : a) * scale;
+// Instruction descriptor of kind::mxf4: e2m1 operands (bits 7, 10), e8m0 scales (bit 23), N / 8
+// at 17, M / 128 at 27; which two bytes of a scale word hold this product's scales: a at 29, b
+// at 4.
+__host__ __device__ constexpr uint32_t idesc_mx4(int M, int N, uint32_t sf_id) {
+  return (1u << 7) | (1u << 10) | (1u << 23) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 29) | (sf_id << 4);
 }
 
-// 64 x 64 outputs per block, 32 of k at a time, 4 x 4 outputs per thread.
-__global__ void __launch_bounds__(256) mx4_linear_kernel(Mx4Args g) {
-  __shared__ float sa[32][kTile + 1], sw[32][kTile + 1];
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const int n0 = blockIdx.x * kTile, tiles = (g.k + 127) / 128;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < g.k; k0 += 32) {
-    for (int i = threadIdx.x; i < 32 * kTile; i += 256) {
-      const int kk = i & 31, r = i >> 5;
-      sa[kk][r] = m0 + r < g.m ? mx4_value((const uint8_t*)g.a, (const uint8_t*)g.a_scales, m0 + r, k0 + kk, g.k, tiles) : 0.0f;
-      sw[kk][r] = n0 + r < g.n ? mx4_value((const uint8_t*)g.w, (const uint8_t*)g.w_scales, n0 + r, k0 + kk, g.k, tiles) : 0.0f;
+// Descriptor of a scale tile for tcgen05.cp: 32 rows of 16 bytes, no swizzle, 128 bytes from one
+// eight rows to the next.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 ld_peer4(uint32_t a, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 p;\n\t"
+      "mapa.shared::cluster.u32 p, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(a), "r"(rank)
+      : "memory");
+  return v;
+}
+
+struct Mx4Params {
+  const float* bias;
+  void* y;
+  int64_t m;
+  int32_t n, k;
+  int32_t n_tiles;  // tiles of features
+  int32_t splits;   // blocks per cluster: parts of k
+  int32_t y_dt;
+  uint32_t* status;
+};
+
+// Four consecutive outputs of a row.
+__device__ __forceinline__ void store4(const Mx4Params& p, int64_t at, float4 v) {
+  if (p.y_dt == DP_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
+        p.y_dt == DP_BF16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
+                          : make_uint2(pack_f16x2_sat(v.x, v.y), pack_f16x2_sat(v.z, v.w));
+}
+
+// ------------------------------------------------------------------ few rows of a
+
+template <int NT>  // tokens per tile
+struct Narrow {
+  static constexpr int RB = NT > 128 ? NT / 128 : 1;  // scale tiles of the tokens
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int A_BYTES = NT * 128;
+  static constexpr int OFF_A = W_BYTES;
+  static constexpr int OFF_SW = OFF_A + A_BYTES;
+  static constexpr int OFF_SA = OFF_SW + 2 * kScaleTile;
+  static constexpr int STAGE = OFF_SA + 2 * kScaleTile * RB;
+  static constexpr int STAGES = 4;
+  static constexpr int PITCH = 128 + 4;  // floats between two tokens of the sums in shared memory
+  static constexpr int SUMS = NT * PITCH * 4;
+  static constexpr int OFF_BAR = STAGES * STAGE > SUMS ? STAGES * STAGE : (SUMS + 15) / 16 * 16;
+  static constexpr int N_BAR = 2 * STAGES + 1;
+  static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+  static constexpr int ALLOC = OFF_MISC + 16 + 1024;
+  static constexpr int SF_COLS = 8 + 8 * RB;  // columns of a step's scales: W's, then the tokens'
+  static constexpr int COL_SF = NT < 32 ? 32 : NT;
+  static constexpr int COLS = COL_SF + 2 * SF_COLS;
+  static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int kThreads = 192;
+  static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(Narrow<NT>::kThreads)
+    mx4_narrow_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                      const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sa, const Mx4Params p) {
+  using L = Narrow<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.splits;
+  const int tile = blockIdx.x / p.splits;
+  const int n_tile = tile % p.n_tiles, m_tile = tile / p.n_tiles;
+  const int steps = (p.k + kStepK - 1) / kStepK;
+  const int per = (steps + p.splits - 1) / p.splits;
+  const int first = rank * per;
+  const int n_loc = max(0, min(per, steps - first));
+
+  const uint32_t bar0 = sb + L::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (L::STAGES + s); };
+  const uint32_t acc_full = bar0 + 8u * (2 * L::STAGES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[kk][ty + 16 * i], sw[kk][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+    mbar_init(acc_full, 1);
+    *abort = 0;
+    fence_mbar_init();
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = m0 + ty + 16 * i;
-      const int c = n0 + tx + 16 * j;
-      if (r >= g.m || c >= g.n) continue;
-      const float v = acc[i][j] + (g.bias ? g.bias[c] : 0.0f);
-      const int64_t at = r * g.n + c;
-      if (g.y_dt == DP_F32) static_cast<float*>(g.y)[at] = v;
-      else if (g.y_dt == DP_BF16) static_cast<uint16_t*>(g.y)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
-      else static_cast<uint16_t*>(g.y)[at] = static_cast<uint16_t>(pack_f16x2_sat(v, 0.0f));
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_sw);
+    tma_prefetch_desc(&tm_sa);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = 0; i < n_loc; ++i) {
+        const int s = i % L::STAGES;
+        if (i >= L::STAGES && !mbar_wait(empty(s), ((i / L::STAGES) - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
+        const uint32_t st = sb + s * L::STAGE;
+        const int kb = first + i;
+        mbar_arrive_expect_tx(full(s), L::STAGE);
+        tma_load_2d(st, &tm_w, kb * 128, n_tile * 128, full(s));
+        tma_load_3d(st + L::OFF_SW, &tm_sw, 0, kb * 2, n_tile, full(s));
+        tma_load_2d(st + L::OFF_A, &tm_a, kb * 128, m_tile * NT, full(s));
+        tma_load_3d(st + L::OFF_SA, &tm_sa, 0, kb * 2, m_tile * NT / 128, full(s));
+        issued = i + 1;
+      }
+      const int from = issued > L::STAGES ? issued - L::STAGES : 0;
+      for (int i = from; i < issued; ++i) mbar_drain_wait(full(i % L::STAGES), (i / L::STAGES) & 1, p.status);
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t dw = sdesc_sw128(sb, 16, 1024);
+      const uint64_t da = sdesc_sw128(sb + L::OFF_A, 16, 1024);
+      for (int i = 0; i < n_loc; ++i) {
+        const int s = i % L::STAGES;
+        if (!mbar_wait(full(s), (i / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV)) break;
+        // the products that read this range of scales are done
+        if (i >= 2 && !mbar_wait(empty((i - 2) % L::STAGES), ((i - 2) / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_S)) break;
+        tc_fence_after();
+        const uint32_t sw = tmem + L::COL_SF + (i & 1) * L::SF_COLS;
+        const uint32_t sa = sw + 8;
+        const uint32_t st = sb + s * L::STAGE;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          cp_scales(sw + c * 4, sdesc_scales(st + L::OFF_SW + c * kScaleTile));
+#pragma unroll
+          for (int r = 0; r < L::RB; ++r)
+            cp_scales(sa + (c * L::RB + r) * 4, sdesc_scales(st + L::OFF_SA + (r * 2 + c) * kScaleTile));
+        }
+        const uint64_t so = static_cast<uint64_t>((s * L::STAGE) >> 4);
+        const int chunks = min(4, (p.k - (first + i) * kStepK + 63) / 64);  // of 64: those behind k are zeros
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks)
+            mma_mx4(tmem, dw + so + c * 2, da + so + c * 2, idesc_mx4(128, NT, (c & 1) * 2), sw + (c >> 1) * 4,
+                    sa + (c >> 1) * 4 * L::RB, (i > 0 || c > 0) ? 1u : 0u);
+        mma_commit(empty(s));
+      }
+      mma_commit(acc_full);
+      mbar_drain_wait(acc_full, 0, p.status);
+    }
+  } else {
+    // one thread per feature: its sums, over the stages, as [token][feature]
+    const int quarter = warp & 3;
+    bool ok = mbar_wait(acc_full, 0, abort, p.status, DEV_ERR_TIMEOUT_O);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      float* dst = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+      const uint32_t src = tmem + ((static_cast<uint32_t>(quarter) * 32u) << 16);
+#pragma unroll 1
+      for (int c0 = 0; c0 < NT; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(src + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c0 + c < NT) dst[(c0 + c) * L::PITCH] = n_loc > 0 ? __uint_as_float(r[c]) : 0.0f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+  if (p.splits > 1) cluster_sync();
+  // this block's share of the tile's tokens x 32 groups of four features
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), p.m - static_cast<int64_t>(m_tile) * NT));
+  const int share = (tokens * 32 + p.splits - 1) / p.splits;
+  const int end = min(tokens * 32, (rank + 1) * share);
+  for (int i = rank * share + threadIdx.x; i < end; i += L::kThreads) {
+    const int f = (i & 31) * 4, col = n_tile * 128 + f, t = i >> 5;
+    if (col >= p.n) continue;
+    float4 v = p.bias ? *reinterpret_cast<const float4*>(p.bias + col) : make_float4(0, 0, 0, 0);
+    const uint32_t at = (t * L::PITCH + f) * 4;
+    if (p.splits == 1) {
+      const float4 x = *reinterpret_cast<const float4*>(smem + at);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    } else {
+      float4 x[kMaxSplits];
+#pragma unroll
+      for (int s = 0; s < kMaxSplits; ++s)
+        if (s < p.splits) x[s] = ld_peer4(sb + at, s);
+#pragma unroll
+      for (int s = 0; s < kMaxSplits; ++s)
+        if (s < p.splits) v.x += x[s].x, v.y += x[s].y, v.z += x[s].z, v.w += x[s].w;
+    }
+    store4(p, (static_cast<int64_t>(m_tile) * NT + t) * p.n + col, v);
+  }
+  if (p.splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+
+// Codes [rows][k / 2] bytes, boxes of 128 bytes by box_rows.
+bool encode_codes(EncodeFn fn, CUtensorMap* t, const void* base, int64_t rows, int32_t k, int box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(k / 2), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(k / 2)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t one[2] = {1, 1};
+  return fn(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale tiles [rows / 128][k / 128][128 words], boxes of two tiles along k by box_rows / 128.
+bool encode_scales(EncodeFn fn, CUtensorMap* t, const void* base, int64_t rows, int32_t k, int box_rows) {
+  const cuuint64_t tiles = static_cast<cuuint64_t>((k + 127) / 128);
+  cuuint64_t dims[3] = {kScaleTile / 4, tiles, static_cast<cuuint64_t>((rows + 127) / 128)};
+  cuuint64_t strides[2] = {kScaleTile, tiles * kScaleTile};
+  cuuint32_t box[3] = {kScaleTile / 4, 2, static_cast<cuuint32_t>(box_rows > 128 ? box_rows / 128 : 1)};
+  cuuint32_t one[3] = {1, 1, 1};
+  return fn(t, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+}
+
+template <int NT>
+cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
+  using L = Narrow<NT>;
+  EncodeFn fn = tensor_map_encoder();
+  CUtensorMap tw, ta, tsw, tsa;
+  if (!fn || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) || !encode_codes(fn, &ta, g.a, g.m, g.k, NT) ||
+      !encode_scales(fn, &tsw, g.w_scales, g.n, g.k, 128) || !encode_scales(fn, &tsa, g.a_scales, g.m, g.k, NT))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> attr_set[64];
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(mx4_narrow_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  Mx4Params p;
+  p.bias = g.bias;
+  p.y = g.y;
+  p.m = g.m;
+  p.n = g.n;
+  p.k = g.k;
+  p.n_tiles = (g.n + 127) / 128;
+  p.y_dt = g.y_dt;
+  p.status = g.status;
+  const int64_t tiles = (g.m + NT - 1) / NT * p.n_tiles;
+  const int steps = (g.k + kStepK - 1) / kStepK;
+  p.splits = 1;
+  while (p.splits < kMaxSplits && tiles * p.splits * 2 <= sms && steps >= p.splits * 2) p.splits *= 2;
+  if (tiles * p.splits > INT_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::ALLOC;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, mx4_narrow_kernel<NT>, tw, ta, tsw, tsa, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s) {
   if (g.m <= 0 || g.n <= 0 || g.n % 8 || g.k <= 0 || g.k % 32) return cudaErrorInvalidValue;
-  const int64_t gy = (g.m + kTile - 1) / kTile;
-  if (gy > 65535) return cudaErrorInvalidValue;
-  mx4_linear_kernel<<<dim3((g.n + kTile - 1) / kTile, static_cast<unsigned>(gy)), 256, 0, s>>>(g);
-  return cudaGetLastError();
+  if (g.m <= 16) return launch_narrow<16>(g, s);
+  if (g.m <= 64) return launch_narrow<64>(g, s);
+  return launch_narrow<128>(g, s);
 }
 
 }  // namespace dp
