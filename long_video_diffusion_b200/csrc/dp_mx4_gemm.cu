@@ -12,6 +12,12 @@
 // features per block), the tokens its N, and k is cut into as many parts as a cluster has blocks,
 // so that all SMs read W at once; the parts are summed through distributed shared memory in a
 // fixed order.
+//
+// Many rows (mx4_wide_kernel): bound by the tensor cores.  A persistent kernel of block pairs,
+// each pair one output tile of 256 x 256 (tcgen05 cta_group::2: a block holds 128 rows of a and
+// 128 of W, and its half of the sums): at 4 bits a product of 64 of k takes 128 clocks and 8 KB
+// of a block's shared memory, half of what it can read and be filled with in that time, where a
+// block by itself would need 12 KB.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -279,6 +285,272 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
   if (p.splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
 }
 
+// ------------------------------------------------------------------ many rows of a
+
+// The forms of the instructions above for a pair of blocks, issued by its first.
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Arrives on `bar` in both blocks once all that this thread issued has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"(static_cast<uint16_t>(3))
+               : "memory");
+}
+
+// Loads into this block's shared memory that signal a barrier of either block of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Shared address `a` of this block in the pair's first block.
+__device__ __forceinline__ uint32_t in_first(uint32_t a) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tensor memory: two accumulators of 256 columns do not fit beside the scales, so they overlap
+// by 64 columns (0-255 and 192-447).  A tile's epilogue reads the shared columns first, which is
+// all that the next tile's products wait for.
+struct Wide {
+  static constexpr int BN = 256;
+  static constexpr int CODES = 128 * 128;  // bytes of a block's rows of a, or of W, per step
+  static constexpr int OFF_B = CODES;
+  static constexpr int OFF_SA = 2 * CODES;
+  static constexpr int OFF_SB = OFF_SA + 2 * kScaleTile;
+  static constexpr int STAGE = OFF_SB + 4 * kScaleTile;
+  static constexpr int STAGES = 6;
+  static constexpr int OFF_BAR = STAGES * STAGE;
+  static constexpr int N_BAR = 2 * STAGES + 5;
+  static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+  static constexpr int ALLOC = OFF_MISC + 16 + 1024;
+  static constexpr int COL_ACC1 = 192;
+  static constexpr int COL_SF = 448;
+  static constexpr int SF_COLS = 24;  // a's 8, then W's 16
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps);
+  static_assert(COL_ACC1 + BN <= COL_SF && COL_SF + 2 * SF_COLS <= 512, "tensor memory budget");
+  static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+struct WideParams {
+  Mx4Params p;
+  int32_t m_tiles, n_tiles, tiles;
+  int32_t group_m;
+};
+
+// Tile t -> (m tile, n tile): groups of group_m m tiles, m fastest inside a group.
+__device__ __forceinline__ void wide_coords(const WideParams& w, int t, int& m_tile, int& n_tile) {
+  const int per_group = w.group_m * w.n_tiles;
+  const int group = t / per_group;
+  const int first_m = group * w.group_m;
+  const int gm = min(w.group_m, w.m_tiles - first_m);
+  const int within = t - group * per_group;
+  m_tile = first_m + within % gm;
+  n_tile = within / gm;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
+    mx4_wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw, const WideParams w) {
+  using L = Wide;
+  const Mx4Params& p = w.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;  // in the pair
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int steps = (p.k + kStepK - 1) / kStepK;
+  const int n_mine = w.tiles > pair ? (w.tiles - pair + pairs - 1) / pairs : 0;
+
+  const uint32_t bar0 = sb + L::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };  // used in the first block only
+  auto empty = [&](int s) { return bar0 + 8u * (L::STAGES + s); };
+  auto acc_full = [&](int b) { return bar0 + 8u * (2 * L::STAGES + b); };
+  auto shared_read = [&](int b) { return bar0 + 8u * (2 * L::STAGES + 2 + b); };  // in the first block only
+  const uint32_t fin = bar0 + 8u * (2 * L::STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(shared_read(b), 2 * L::kEpiWarps);
+    }
+    mbar_init(fin, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_sa);
+    tma_prefetch_desc(&tm_sw);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < n_mine; ++i) {
+        int m_tile, n_tile;
+        wide_coords(w, pair + i * pairs, m_tile, n_tile);
+        for (int kt = 0; kt < steps; ++kt, ++g) {
+          const int s = g % L::STAGES;
+          if (g >= L::STAGES && !mbar_wait(empty(s), ((g / L::STAGES) - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = sb + s * L::STAGE;
+          const uint32_t bar = in_first(full(s));
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * L::STAGE);
+          tma_load_2d_pair(st, &tm_a, kt * 128, m_tile * 256 + rank * 128, bar);
+          tma_load_2d_pair(st + L::OFF_B, &tm_w, kt * 128, n_tile * 256 + rank * 128, bar);
+          tma_load_3d_pair(st + L::OFF_SA, &tm_sa, 0, kt * 2, m_tile * 2 + rank, bar);
+          tma_load_3d_pair(st + L::OFF_SB, &tm_sw, 0, kt * 2, n_tile * 2, bar);
+        }
+      }
+      // both blocks' copies land before either's shared memory is released (the second waits for
+      // the first at the end)
+      if (rank == 0)
+        for (int i = max(0, g - L::STAGES); i < g; ++i) mbar_drain_wait(full(i % L::STAGES), (i / L::STAGES) & 1, p.status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer of the pair
+    if (rank == 0 && lane == 0) {
+      const uint64_t da = sdesc_sw128(sb, 16, 1024);
+      const uint64_t db = sdesc_sw128(sb + L::OFF_B, 16, 1024);
+      bool ok = true;
+      int g = 0;
+      for (int i = 0; ok && i < n_mine; ++i) {
+        // the tile before has left the shared columns (and the one before that its own)
+        if (i >= 1 && !mbar_wait(shared_read((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (i & 1) * L::COL_ACC1;
+        for (int kt = 0; kt < steps; ++kt, ++g) {
+          const int s = g % L::STAGES;
+          ok = mbar_wait(full(s), (g / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV) &&
+               (g < 2 || mbar_wait(empty((g - 2) % L::STAGES), ((g - 2) / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_S));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = tmem + L::COL_SF + (g & 1) * L::SF_COLS;
+          const uint32_t sw = sa + 8;
+          const uint32_t st = sb + s * L::STAGE;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            cp_scales_pair(sa + c * 4, sdesc_scales(st + L::OFF_SA + c * kScaleTile));
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              cp_scales_pair(sw + (c * 2 + r) * 4, sdesc_scales(st + L::OFF_SB + (r * 2 + c) * kScaleTile));
+          }
+          const uint64_t so = static_cast<uint64_t>((s * L::STAGE) >> 4);
+          const int chunks = min(4, (p.k - kt * kStepK + 63) / 64);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < chunks)
+              mma_mx4_pair(d, da + so + c * 2, db + so + c * 2, idesc_mx4(256, L::BN, (c & 1) * 2), sa + (c >> 1) * 4,
+                           sw + (c >> 1) * 8, (kt > 0 || c > 0) ? 1u : 0u);
+          commit_pair(empty(s));
+        }
+        if (ok) commit_pair(acc_full(i & 1));
+      }
+      commit_pair(fin);
+      mbar_drain_wait(fin, 0, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue: one thread per row
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;  // which of each two chunks of 32 columns
+    const uint32_t tlane = (static_cast<uint32_t>(quarter) * 32u) << 16;
+    const uint32_t read0 = in_first(shared_read(0)), read1 = in_first(shared_read(1));
+    for (int i = 0; i < n_mine; ++i) {
+      const int b = i & 1;
+      bool ok = mbar_wait(acc_full(b), (i >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      int m_tile, n_tile;
+      wide_coords(w, pair + i * pairs, m_tile, n_tile);
+      const int64_t row = static_cast<int64_t>(m_tile) * 256 + rank * 128 + quarter * 32 + lane;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        // the shared columns first: the last ones of accumulator 0, the first ones of 1
+        const int c0 = ((b ? j : 3 - j) * 2 + half) * 32;
+        uint32_t r[32];
+        tmem_ld32(tmem + tlane + b * L::COL_ACC1 + c0, r);
+        tmem_wait_ld();
+        if (j == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(b ? read1 : read0);
+        }
+        const int col = n_tile * L::BN + c0;
+        if (row < p.m) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            if (col + c >= p.n) break;
+            float4 v = make_float4(__uint_as_float(r[c]), __uint_as_float(r[c + 1]), __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+            if (p.bias) {
+              const float4 x = *reinterpret_cast<const float4*>(p.bias + col + c);
+              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            store4(p, row * p.n + col + c, v);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing of the pair is in flight
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+  cluster_sync();
+}
+
 // ------------------------------------------------------------------ host
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
@@ -359,10 +631,62 @@ cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
+  using L = Wide;
+  EncodeFn fn = tensor_map_encoder();
+  CUtensorMap ta, tw, tsa, tsw;
+  if (!fn || !encode_codes(fn, &ta, g.a, g.m, g.k, 128) || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) ||
+      !encode_scales(fn, &tsa, g.a_scales, g.m, g.k, 128) || !encode_scales(fn, &tsw, g.w_scales, g.n, g.k, 256))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> pairs_of[64];  // pairs that fit on the device at once
+  int most = pairs_of[dev].load(std::memory_order_acquire);
+  if (!most) {
+    e = cudaFuncSetAttribute(mx4_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::ALLOC;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&most, mx4_wide_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (most < 1) return cudaErrorInvalidConfiguration;
+    pairs_of[dev].store(most, std::memory_order_release);
+  }
+  WideParams w;
+  w.p.bias = g.bias;
+  w.p.y = g.y;
+  w.p.m = g.m;
+  w.p.n = g.n;
+  w.p.k = g.k;
+  w.p.n_tiles = 0;
+  w.p.splits = 1;
+  w.p.y_dt = g.y_dt;
+  w.p.status = g.status;
+  const int64_t m_tiles = (g.m + 255) / 256, n_tiles = (g.n + 255) / 256;
+  if (m_tiles * n_tiles > INT_MAX) return cudaErrorInvalidValue;
+  w.m_tiles = static_cast<int32_t>(m_tiles);
+  w.n_tiles = static_cast<int32_t>(n_tiles);
+  w.tiles = w.m_tiles * w.n_tiles;
+  w.group_m = 8;
+  const int pairs = w.tiles < most ? w.tiles : most;
+  mx4_wide_kernel<<<2 * pairs, L::kThreads, L::ALLOC, s>>>(ta, tw, tsa, tsw, w);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s) {
   if (g.m <= 0 || g.n <= 0 || g.n % 8 || g.k <= 0 || g.k % 32) return cudaErrorInvalidValue;
+  if (g.m > 256) return launch_wide(g, s);
   if (g.m <= 16) return launch_narrow<16>(g, s);
   if (g.m <= 64) return launch_narrow<64>(g, s);
   return launch_narrow<128>(g, s);
