@@ -5,8 +5,8 @@
 //
 // A step is 256 of k: TMA brings the codes' tiles and the scales' (whose layout in memory, tiles
 // of 128 rows by 128 columns in 512 bytes, is the one tcgen05.cp spreads over tensor memory);
-// what lies behind k or behind the last row arrives as zeros.  Scales alternate between two
-// column ranges of tensor memory, so that a step's copy never meets the step before's products.
+// what lies behind k or behind the last row arrives as zeros.  Scales go round several column
+// ranges of tensor memory, so that a step's copy never meets an earlier step's products.
 //
 // Few rows of a (mx4_narrow_kernel): bound by reading W once.  W's rows are the tile's M (128
 // features per block), the tokens its N, and k is cut into as many parts as a cluster has blocks,
@@ -129,7 +129,7 @@ struct Narrow {
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
   static constexpr int SF_COLS = 8 + 8 * RB;  // columns of a step's scales: W's, then the tokens'
   static constexpr int COL_SF = NT < 32 ? 32 : NT;
-  static constexpr int COLS = COL_SF + 2 * SF_COLS;
+  static constexpr int COLS = COL_SF + STAGES * SF_COLS;  // a range of scales per stage
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr int kThreads = 192;
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
@@ -207,10 +207,8 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
       for (int i = 0; i < n_loc; ++i) {
         const int s = i % L::STAGES;
         if (!mbar_wait(full(s), (i / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV)) break;
-        // the products that read this range of scales are done
-        if (i >= 2 && !mbar_wait(empty((i - 2) % L::STAGES), ((i - 2) / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_S)) break;
         tc_fence_after();
-        const uint32_t sw = tmem + L::COL_SF + (i & 1) * L::SF_COLS;
+        const uint32_t sw = tmem + L::COL_SF + s * L::SF_COLS;
         const uint32_t sa = sw + 8;
         const uint32_t st = sb + s * L::STAGE;
 #pragma unroll
@@ -337,8 +335,9 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 }
 
 // Tensor memory: two accumulators of 256 columns do not fit beside the scales, so they overlap
-// by 64 columns (0-255 and 192-447).  A tile's epilogue reads the shared columns first, which is
-// all that the next tile's products wait for.
+// by 96 columns (0-255 and 160-415).  A tile's epilogue reads the shared columns first, which is
+// all that the next tile's products wait for.  Two ranges of scales instead of four let only one
+// step wait behind the one that runs: 12480 x 11008 x 4096 took 385 us with two.
 struct Wide {
   static constexpr int BN = 256;
   static constexpr int CODES = 128 * 128;  // bytes of a block's rows of a, or of W, per step
@@ -346,17 +345,21 @@ struct Wide {
   static constexpr int OFF_SA = 2 * CODES;
   static constexpr int OFF_SB = OFF_SA + 2 * kScaleTile;
   static constexpr int STAGE = OFF_SB + 4 * kScaleTile;
-  static constexpr int STAGES = 6;
-  static constexpr int OFF_BAR = STAGES * STAGE;
+  static constexpr int STAGES = 5;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps);
+  static constexpr int OUT_BYTES = 32 * 128;  // an epilogue warp's 32 rows of 128 bytes of output
+  static constexpr int OFF_OUT = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_OUT + kEpiWarps * OUT_BYTES;
   static constexpr int N_BAR = 2 * STAGES + 5;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  static constexpr int COL_ACC1 = 192;
-  static constexpr int COL_SF = 448;
+  static constexpr int COL_ACC1 = 160;
+  static constexpr int COL_SF = 416;
   static constexpr int SF_COLS = 24;  // a's 8, then W's 16
-  static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = 32 * (2 + kEpiWarps);
-  static_assert(COL_ACC1 + BN <= COL_SF && COL_SF + 2 * SF_COLS <= 512, "tensor memory budget");
+  static constexpr int SF_RANGES = 4;
+  static_assert(COL_ACC1 + BN <= COL_SF && COL_SF + SF_RANGES * SF_COLS <= 512, "tensor memory budget");
+  static_assert(COL_ACC1 >= 128, "the shared columns lie in the two groups of 64 read first");
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 };
 
@@ -379,7 +382,8 @@ __device__ __forceinline__ void wide_coords(const WideParams& w, int t, int& m_t
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     mx4_wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw, const WideParams w) {
+                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw,
+                    const __grid_constant__ CUtensorMap tm_y, const WideParams w) {
   using L = Wide;
   const Mx4Params& p = w.p;
   extern __shared__ uint8_t smem_raw[];
@@ -471,10 +475,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
         for (int kt = 0; kt < steps; ++kt, ++g) {
           const int s = g % L::STAGES;
           ok = mbar_wait(full(s), (g / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV) &&
-               (g < 2 || mbar_wait(empty((g - 2) % L::STAGES), ((g - 2) / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_S));
+               (g < L::SF_RANGES || mbar_wait(empty((g - L::SF_RANGES) % L::STAGES), ((g - L::SF_RANGES) / L::STAGES) & 1, abort,
+                                              p.status, DEV_ERR_TIMEOUT_S));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = tmem + L::COL_SF + (g & 1) * L::SF_COLS;
+          const uint32_t sa = tmem + L::COL_SF + (g % L::SF_RANGES) * L::SF_COLS;
           const uint32_t sw = sa + 8;
           const uint32_t st = sb + s * L::STAGE;
 #pragma unroll
@@ -500,10 +505,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue: one thread per row
+    // A warp's 32 rows by 128 bytes go through shared memory (128-byte swizzle) to a TMA store,
+    // which writes whole lines and leaves out what lies behind m or n.
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;  // which of each two chunks of 32 columns
+    const int half = (warp - 2) >> 2;
     const uint32_t tlane = (static_cast<uint32_t>(quarter) * 32u) << 16;
     const uint32_t read0 = in_first(shared_read(0)), read1 = in_first(shared_read(1));
+    uint8_t* stage = smem + L::OFF_OUT + (warp - 2) * L::OUT_BYTES;
+    auto put = [&](const uint32_t (&wd)[32], int64_t row0, int col) {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the store before has read it
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(wd[4 * c], wd[4 * c + 1], wd[4 * c + 2], wd[4 * c + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && row0 < p.m && col < p.n) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(&tm_y)),
+                     "r"(smem_u32(stage)), "r"(col), "r"(static_cast<int32_t>(row0))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    };
     for (int i = 0; i < n_mine; ++i) {
       const int b = i & 1;
       bool ok = mbar_wait(acc_full(b), (i >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
@@ -512,13 +535,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       tc_fence_after();
       int m_tile, n_tile;
       wide_coords(w, pair + i * pairs, m_tile, n_tile);
-      const int64_t row = static_cast<int64_t>(m_tile) * 256 + rank * 128 + quarter * 32 + lane;
+      const int64_t row0 = static_cast<int64_t>(m_tile) * 256 + rank * 128 + quarter * 32;
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        // the shared columns first: the last ones of accumulator 0, the first ones of 1
-        const int c0 = ((b ? j : 3 - j) * 2 + half) * 32;
-        uint32_t r[32];
-        tmem_ld32(tmem + tlane + b * L::COL_ACC1 + c0, r);
+      for (int j = 0; j < 2; ++j) {
+        // groups of 64 columns, those with shared columns first: 3 and 2 of accumulator 0, 0 and 1 of 1
+        const int c0 = (b ? 2 * j + half : 3 - 2 * j - half) * 64;
+        uint32_t r[2][32];
+        tmem_ld32(tmem + tlane + b * L::COL_ACC1 + c0, r[0]);
+        tmem_ld32(tmem + tlane + b * L::COL_ACC1 + c0 + 32, r[1]);
         tmem_wait_ld();
         if (j == 0) {
           tc_fence_before();
@@ -526,20 +550,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
           if (lane == 0) arrive_cluster(b ? read1 : read0);
         }
         const int col = n_tile * L::BN + c0;
-        if (row < p.m) {
+        if (p.bias) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            if (col + c >= p.n) break;
-            float4 v = make_float4(__uint_as_float(r[c]), __uint_as_float(r[c + 1]), __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
-            if (p.bias) {
+          for (int c = 0; c < 64; c += 4)
+            if (col + c < p.n) {
               const float4 x = *reinterpret_cast<const float4*>(p.bias + col + c);
-              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+              uint32_t* v = &r[c >> 5][c & 31];
+              v[0] = __float_as_uint(__uint_as_float(v[0]) + x.x);
+              v[1] = __float_as_uint(__uint_as_float(v[1]) + x.y);
+              v[2] = __float_as_uint(__uint_as_float(v[2]) + x.z);
+              v[3] = __float_as_uint(__uint_as_float(v[3]) + x.w);
             }
-            store4(p, row * p.n + col + c, v);
+        }
+        if (p.y_dt == DP_F32) {
+          put(r[0], row0, col);
+          put(r[1], row0, col + 32);
+        } else {
+          uint32_t wd[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float lo = __uint_as_float(r[c >> 4][(2 * c) & 31]), hi = __uint_as_float(r[c >> 4][(2 * c + 1) & 31]);
+            wd[c] = p.y_dt == DP_BF16 ? pack_bf16x2(lo, hi) : pack_f16x2_sat(lo, hi);
           }
+          put(wd, row0, col);
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -576,6 +613,19 @@ bool encode_scales(EncodeFn fn, CUtensorMap* t, const void* base, int64_t rows, 
   return fn(t, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [m][n], boxes of 32 rows by 128 bytes.
+bool encode_out(EncodeFn fn, CUtensorMap* t, void* y, int64_t m, int32_t n, dp_dtype dt) {
+  const int eb = dt == DP_F32 ? 4 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(n) * eb};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / eb), 32};
+  cuuint32_t one[2] = {1, 1};
+  const CUtensorMapDataType type = dt == DP_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dt == DP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(t, type, 2, y, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t device_sms(int* dev, int* sms) {
@@ -634,8 +684,8 @@ cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
 cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
   using L = Wide;
   EncodeFn fn = tensor_map_encoder();
-  CUtensorMap ta, tw, tsa, tsw;
-  if (!fn || !encode_codes(fn, &ta, g.a, g.m, g.k, 128) || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) ||
+  CUtensorMap ta, tw, tsa, tsw, ty;
+  if (!fn || !encode_out(fn, &ty, g.y, g.m, g.n, g.y_dt) || !encode_codes(fn, &ta, g.a, g.m, g.k, 128) || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) ||
       !encode_scales(fn, &tsa, g.a_scales, g.m, g.k, 128) || !encode_scales(fn, &tsw, g.w_scales, g.n, g.k, 256))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
@@ -678,7 +728,7 @@ cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
   w.tiles = w.m_tiles * w.n_tiles;
   w.group_m = 8;
   const int pairs = w.tiles < most ? w.tiles : most;
-  mx4_wide_kernel<<<2 * pairs, L::kThreads, L::ALLOC, s>>>(ta, tw, tsa, tsw, w);
+  mx4_wide_kernel<<<2 * pairs, L::kThreads, L::ALLOC, s>>>(ta, tw, tsa, tsw, ty, w);
   return cudaGetLastError();
 }
 
