@@ -335,9 +335,8 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 }
 
 // Tensor memory: two accumulators of 256 columns do not fit beside the scales, so they overlap
-// by 96 columns (0-255 and 160-415).  A tile's epilogue reads the shared columns first, which is
-// all that the next tile's products wait for.  Two ranges of scales instead of four let only one
-// step wait behind the one that runs: 12480 x 11008 x 4096 took 385 us with two.
+// by half (0-255 and 128-383).  A tile's epilogue reads the shared columns first, which is all
+// that the next tile's products wait for.  Every stage has a range of columns for its scales.
 struct Wide {
   static constexpr int BN = 256;
   static constexpr int CODES = 128 * 128;  // bytes of a block's rows of a, or of W, per step
@@ -354,11 +353,10 @@ struct Wide {
   static constexpr int N_BAR = 2 * STAGES + 5;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  static constexpr int COL_ACC1 = 160;
-  static constexpr int COL_SF = 416;
+  static constexpr int COL_ACC1 = 128;
+  static constexpr int COL_SF = 384;
   static constexpr int SF_COLS = 24;  // a's 8, then W's 16
-  static constexpr int SF_RANGES = 4;
-  static_assert(COL_ACC1 + BN <= COL_SF && COL_SF + SF_RANGES * SF_COLS <= 512, "tensor memory budget");
+  static_assert(COL_ACC1 + BN <= COL_SF && COL_SF + STAGES * SF_COLS <= 512, "tensor memory budget");
   static_assert(COL_ACC1 >= 128, "the shared columns lie in the two groups of 64 read first");
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 };
@@ -462,43 +460,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer of the pair
-    if (rank == 0 && lane == 0) {
+    // One thread, whose own instructions have to stay ahead of the tensor cores' 512 clocks per
+    // step: the ring is unrolled, so that addresses and descriptors are constants off a base.
+    if (rank == 0 && lane == 0 && n_mine > 0) {
       const uint64_t da = sdesc_sw128(sb, 16, 1024);
       const uint64_t db = sdesc_sw128(sb + L::OFF_B, 16, 1024);
-      bool ok = true;
-      int g = 0;
-      for (int i = 0; ok && i < n_mine; ++i) {
-        // the tile before has left the shared columns (and the one before that its own)
-        if (i >= 1 && !mbar_wait(shared_read((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (i & 1) * L::COL_ACC1;
-        for (int kt = 0; kt < steps; ++kt, ++g) {
-          const int s = g % L::STAGES;
-          ok = mbar_wait(full(s), (g / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV) &&
-               (g < L::SF_RANGES || mbar_wait(empty((g - L::SF_RANGES) % L::STAGES), ((g - L::SF_RANGES) / L::STAGES) & 1, abort,
-                                              p.status, DEV_ERR_TIMEOUT_S));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sa = tmem + L::COL_SF + (g % L::SF_RANGES) * L::SF_COLS;
-          const uint32_t sw = sa + 8;
-          const uint32_t st = sb + s * L::STAGE;
+      const uint64_t dsa = sdesc_scales(sb + L::OFF_SA);
+      const uint64_t dsb = sdesc_scales(sb + L::OFF_SB);
+      const int last_chunks = (p.k - (steps - 1) * kStepK + 63) / 64;  // of 64, in a tile's last step
+      uint32_t parity = 0;
+      int i = 0, kt = 0;
+      bool more = true;
+      while (more) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            cp_scales_pair(sa + c * 4, sdesc_scales(st + L::OFF_SA + c * kScaleTile));
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              cp_scales_pair(sw + (c * 2 + r) * 4, sdesc_scales(st + L::OFF_SB + (r * 2 + c) * kScaleTile));
+        for (int s = 0; s < L::STAGES; ++s) {
+          if (!more) break;
+          // the tile before has left the shared columns (and the one before that its own)
+          if (kt == 0 && i >= 1 && !mbar_wait(shared_read((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O)) {
+            more = false;
+            break;
           }
-          const uint64_t so = static_cast<uint64_t>((s * L::STAGE) >> 4);
-          const int chunks = min(4, (p.k - kt * kStepK + 63) / 64);
+          if (!mbar_wait(full(s), parity, abort, p.status, DEV_ERR_TIMEOUT_KV)) {
+            more = false;
+            break;
+          }
+          tc_fence_after();
+          constexpr uint32_t kStage16 = L::STAGE >> 4;
+          const uint32_t d = tmem + (i & 1) * L::COL_ACC1;
+          const uint32_t sa = tmem + L::COL_SF + s * L::SF_COLS;
+          const uint32_t sw = sa + 8;
+          const int chunks = kt == steps - 1 ? last_chunks : 4;
+          const uint32_t go_on = kt > 0 ? 1u : 0u;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < chunks)
-              mma_mx4_pair(d, da + so + c * 2, db + so + c * 2, idesc_mx4(256, L::BN, (c & 1) * 2), sa + (c >> 1) * 4,
-                           sw + (c >> 1) * 8, (kt > 0 || c > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {  // 128 of k: its scales, then its products
+            if (2 * h >= chunks) break;
+            cp_scales_pair(sa + h * 4, sdesc_add(dsa, s * kStage16 + h * (kScaleTile >> 4)));
+            cp_scales_pair(sw + h * 8, sdesc_add(dsb, s * kStage16 + h * (kScaleTile >> 4)));
+            cp_scales_pair(sw + h * 8 + 4, sdesc_add(dsb, s * kStage16 + (2 + h) * (kScaleTile >> 4)));
+          }
+          mma_mx4_pair(d, sdesc_add(da, s * kStage16), sdesc_add(db, s * kStage16), idesc_mx4(256, L::BN, 0), sa, sw, go_on);
+          if (chunks > 1) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 2), sdesc_add(db, s * kStage16 + 2), idesc_mx4(256, L::BN, 2), sa, sw, 1u);
+          if (chunks > 2) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 4), sdesc_add(db, s * kStage16 + 4), idesc_mx4(256, L::BN, 0), sa + 4, sw + 8, 1u);
+          if (chunks > 3) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 6), sdesc_add(db, s * kStage16 + 6), idesc_mx4(256, L::BN, 2), sa + 4, sw + 8, 1u);
           commit_pair(empty(s));
+          if (++kt == steps) {
+            commit_pair(acc_full(i & 1));
+            kt = 0;
+            more = ++i < n_mine;
+          }
         }
-        if (ok) commit_pair(acc_full(i & 1));
+        parity ^= 1;
       }
       commit_pair(fin);
       mbar_drain_wait(fin, 0, p.status);
