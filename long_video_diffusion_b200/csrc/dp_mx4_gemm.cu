@@ -299,6 +299,17 @@ __device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 // Arrives on `bar` in both blocks once all that this thread issued has completed.
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
@@ -460,9 +471,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer of the pair
-    // One thread, whose own instructions have to stay ahead of the tensor cores' 512 clocks per
-    // step: the ring is unrolled, so that addresses and descriptors are constants off a base.
-    if (rank == 0 && lane == 0 && n_mine > 0) {
+    // The warp's own instructions have to stay ahead of the tensor cores' 512 clocks per step: it
+    // runs the loop as a whole (uniform control flow and operands) and elects one lane for the
+    // tensor-core instructions; the ring is unrolled, so that addresses are constants off a base.
+    if (rank == 0 && n_mine > 0) {
       const uint64_t da = sdesc_sw128(sb, 16, 1024);
       const uint64_t db = sdesc_sw128(sb + L::OFF_B, 16, 1024);
       const uint64_t dsa = sdesc_scales(sb + L::OFF_SA);
@@ -475,12 +487,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
         for (int s = 0; s < L::STAGES; ++s) {
           if (!more) break;
+          bool ok = true;
           // the tile before has left the shared columns (and the one before that its own)
-          if (kt == 0 && i >= 1 && !mbar_wait(shared_read((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O)) {
-            more = false;
-            break;
-          }
-          if (!mbar_wait(full(s), parity, abort, p.status, DEV_ERR_TIMEOUT_KV)) {
+          if (kt == 0 && i >= 1) ok = mbar_wait(shared_read((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_O);
+          ok = ok && mbar_wait(full(s), parity, abort, p.status, DEV_ERR_TIMEOUT_KV);
+          if (!__all_sync(0xffffffffu, ok)) {
             more = false;
             break;
           }
@@ -491,28 +502,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
           const uint32_t sw = sa + 8;
           const int chunks = kt == steps - 1 ? last_chunks : 4;
           const uint32_t go_on = kt > 0 ? 1u : 0u;
+          const bool tile_done = kt == steps - 1;
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 128 of k: its scales, then its products
-            if (2 * h >= chunks) break;
-            cp_scales_pair(sa + h * 4, sdesc_add(dsa, s * kStage16 + h * (kScaleTile >> 4)));
-            cp_scales_pair(sw + h * 8, sdesc_add(dsb, s * kStage16 + h * (kScaleTile >> 4)));
-            cp_scales_pair(sw + h * 8 + 4, sdesc_add(dsb, s * kStage16 + (2 + h) * (kScaleTile >> 4)));
+            for (int h = 0; h < 2; ++h) {  // 128 of k: its scales
+              if (2 * h >= chunks) break;
+              cp_scales_pair(sa + h * 4, sdesc_add(dsa, s * kStage16 + h * (kScaleTile >> 4)));
+              cp_scales_pair(sw + h * 8, sdesc_add(dsb, s * kStage16 + h * (kScaleTile >> 4)));
+              cp_scales_pair(sw + h * 8 + 4, sdesc_add(dsb, s * kStage16 + (2 + h) * (kScaleTile >> 4)));
+            }
+            mma_mx4_pair(d, sdesc_add(da, s * kStage16), sdesc_add(db, s * kStage16), idesc_mx4(256, L::BN, 0), sa, sw, go_on);
+            if (chunks > 1) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 2), sdesc_add(db, s * kStage16 + 2), idesc_mx4(256, L::BN, 2), sa, sw, 1u);
+            if (chunks > 2) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 4), sdesc_add(db, s * kStage16 + 4), idesc_mx4(256, L::BN, 0), sa + 4, sw + 8, 1u);
+            if (chunks > 3) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 6), sdesc_add(db, s * kStage16 + 6), idesc_mx4(256, L::BN, 2), sa + 4, sw + 8, 1u);
+            commit_pair(empty(s));
+            if (tile_done) commit_pair(acc_full(i & 1));
           }
-          mma_mx4_pair(d, sdesc_add(da, s * kStage16), sdesc_add(db, s * kStage16), idesc_mx4(256, L::BN, 0), sa, sw, go_on);
-          if (chunks > 1) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 2), sdesc_add(db, s * kStage16 + 2), idesc_mx4(256, L::BN, 2), sa, sw, 1u);
-          if (chunks > 2) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 4), sdesc_add(db, s * kStage16 + 4), idesc_mx4(256, L::BN, 0), sa + 4, sw + 8, 1u);
-          if (chunks > 3) mma_mx4_pair(d, sdesc_add(da, s * kStage16 + 6), sdesc_add(db, s * kStage16 + 6), idesc_mx4(256, L::BN, 2), sa + 4, sw + 8, 1u);
-          commit_pair(empty(s));
-          if (++kt == steps) {
-            commit_pair(acc_full(i & 1));
+          __syncwarp();
+          ++kt;
+          if (tile_done) {
             kt = 0;
             more = ++i < n_mine;
           }
         }
         parity ^= 1;
       }
-      commit_pair(fin);
-      mbar_drain_wait(fin, 0, p.status);
+      if (elect_one()) {
+        commit_pair(fin);
+        mbar_drain_wait(fin, 0, p.status);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue: one thread per row
