@@ -201,35 +201,42 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
       for (int i = from; i < issued; ++i) mbar_drain_wait(full(i % L::STAGES), (i / L::STAGES) & 1, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t dw = sdesc_sw128(sb, 16, 1024);
-      const uint64_t da = sdesc_sw128(sb + L::OFF_A, 16, 1024);
-      for (int i = 0; i < n_loc; ++i) {
-        const int s = i % L::STAGES;
-        if (!mbar_wait(full(s), (i / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV)) break;
-        tc_fence_after();
-        const uint32_t sw = tmem + L::COL_SF + s * L::SF_COLS;
-        const uint32_t sa = sw + 8;
-        const uint32_t st = sb + s * L::STAGE;
+    // the whole warp, one lane elected for the tensor-core instructions (see mx4_wide_kernel)
+    const uint64_t dw = sdesc_sw128(sb, 16, 1024);
+    const uint64_t da = sdesc_sw128(sb + L::OFF_A, 16, 1024);
+    const uint64_t dsw = sdesc_scales(sb + L::OFF_SW);
+    const uint64_t dsa = sdesc_scales(sb + L::OFF_SA);
+    for (int i = 0; i < n_loc; ++i) {
+      const int s = i % L::STAGES;
+      const bool ok = mbar_wait(full(s), (i / L::STAGES) & 1, abort, p.status, DEV_ERR_TIMEOUT_KV);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t sw = tmem + L::COL_SF + s * L::SF_COLS;
+      const uint32_t sa = sw + 8;
+      const uint32_t so = (s * L::STAGE) >> 4;
+      const int chunks = min(4, (p.k - (first + i) * kStepK + 63) / 64);  // of 64: those behind k are zeros
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          cp_scales(sw + c * 4, sdesc_scales(st + L::OFF_SW + c * kScaleTile));
+          cp_scales(sw + c * 4, sdesc_add(dsw, so + c * (kScaleTile >> 4)));
 #pragma unroll
           for (int r = 0; r < L::RB; ++r)
-            cp_scales(sa + (c * L::RB + r) * 4, sdesc_scales(st + L::OFF_SA + (r * 2 + c) * kScaleTile));
+            cp_scales(sa + (c * L::RB + r) * 4, sdesc_add(dsa, so + (r * 2 + c) * (kScaleTile >> 4)));
         }
-        const uint64_t so = static_cast<uint64_t>((s * L::STAGE) >> 4);
-        const int chunks = min(4, (p.k - (first + i) * kStepK + 63) / 64);  // of 64: those behind k are zeros
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (c < chunks)
-            mma_mx4(tmem, dw + so + c * 2, da + so + c * 2, idesc_mx4(128, NT, (c & 1) * 2), sw + (c >> 1) * 4,
+            mma_mx4(tmem, sdesc_add(dw, so + c * 2), sdesc_add(da, so + c * 2), idesc_mx4(128, NT, (c & 1) * 2), sw + (c >> 1) * 4,
                     sa + (c >> 1) * 4 * L::RB, (i > 0 || c > 0) ? 1u : 0u);
         mma_commit(empty(s));
       }
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(acc_full);
       mbar_drain_wait(acc_full, 0, p.status);
     }
+    __syncwarp();
   } else {
     // one thread per feature: its sums, over the stages, as [token][feature]
     const int quarter = warp & 3;
@@ -297,17 +304,6 @@ __device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b,
 
 __device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-// One lane of a converged warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(yes));
-  return yes != 0;
 }
 
 // Arrives on `bar` in both blocks once all that this thread issued has completed.

@@ -259,8 +259,10 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
           mbar_drain_wait(v_full(j % L::STAGES), (j / L::STAGES) & 1, p.status);
         }
       }
-    } else if (lane == 0) {
+    } else {
       // ------------------------------------------------------------ MMA issuers
+      // Each warp runs its loop as a whole and elects one lane for the tensor-core instructions:
+      // with uniform operands the issue stays ahead of the products.
       constexpr uint32_t idS = idesc_f32acc(Operand<F16>::kFmt, BM, BN, false);
       constexpr uint32_t idPV = idesc_f32acc(Operand<F16>::kFmt, BM, HD, true);
       auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
@@ -270,38 +272,46 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
       const uint64_t dk0 = sdesc_sw128(sb + L::OFF_K, 16, 1024);
       const uint64_t dv0 = sdesc_sw128(sb + L::OFF_V, L::KV_CHUNK, 1024);
       bool ok = wait(q_full(0), 0, DEV_ERR_TIMEOUT_Q) && wait(q_full(1), 0, DEV_ERR_TIMEOUT_Q);
+      ok = __all_sync(0xffffffffu, ok);
       // S_g of tile t, once K_t is there and S_g of tile t - 1 is in the softmax's registers
       auto do_s = [&](int t, int g) {
         const int st = t % L::STAGES;
         ok = (t == 0 || wait(s_free(g), (t - 1) & 1, DEV_ERR_TIMEOUT_S)) &&
              wait(k_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t dq = dq0 + static_cast<uint64_t>((g * L::Q_BYTES) >> 4);
-        const uint64_t dk = dk0 + static_cast<uint64_t>((st * L::KV_BYTES) >> 4);
+        const uint64_t dq = sdesc_add(dq0, (g * L::Q_BYTES) >> 4);
+        const uint64_t dk = sdesc_add(dk0, (st * L::KV_BYTES) >> 4);
         const uint32_t d = tmem + L::COL_S + g * BN;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t oq = static_cast<uint64_t>(((kk >> 2) * L::Q_CHUNK + (kk & 3) * 32) >> 4);
-          const uint64_t ok_ = static_cast<uint64_t>(((kk >> 2) * L::KV_CHUNK + (kk & 3) * 32) >> 4);
-          mma_ss(d, dq + oq, dk + ok_, idS, kk > 0);
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_ss(d, sdesc_add(dq, ((kk >> 2) * L::Q_CHUNK + (kk & 3) * 32) >> 4),
+                   sdesc_add(dk, ((kk >> 2) * L::KV_CHUNK + (kk & 3) * 32) >> 4), idS, kk > 0);
+          mma_commit(s_full(g));
         }
-        mma_commit(s_full(g));
+        __syncwarp();
       };
-      // O_g += P_g V of tile t
-      auto do_pv = [&](int t, int g) {
+      // O_g += P_g V of tile t; `done`: the tile's last product, which frees the stage
+      auto do_pv = [&](int t, int g, bool done) {
         const int st = t % L::STAGES;
         ok = wait(p_full(g), t & 1, DEV_ERR_TIMEOUT_P) && wait(v_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV) &&
              (!tail || t != n_loc - 1 || wait(v_fixed, 0, DEV_ERR_TIMEOUT_KV));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t dv = dv0 + static_cast<uint64_t>((st * L::KV_BYTES) >> 4);
+        const uint64_t dv = sdesc_add(dv0, (st * L::KV_BYTES) >> 4);
         const uint32_t pa = tmem + L::COL_P + g * (BN / 2);
         const uint32_t d = tmem + L::COL_O + g * HD;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(d, pa + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idPV, (t > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(o_done(g));
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(d, pa + kk * 8, sdesc_add(dv, (kk * 2048) >> 4), idPV, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(o_done(g));
+          if (done) mma_commit(kv_empty(st));
+        }
+        __syncwarp();
       };
       const int iw = warp - L::W_ISS;
       if constexpr (L::S_PER_TILE) {
@@ -310,9 +320,8 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
           for (int t = 0; ok && t < n; ++t) do_s(t, iw);
         } else {
           for (int t = 0; ok && t < n_loc; ++t) {
-            if (t < nt[0]) do_pv(t, 0);
-            if (ok && t < nt[1]) do_pv(t, 1);
-            if (ok) mma_commit(kv_empty(t % L::STAGES));
+            if (t < nt[0]) do_pv(t, 0, t >= nt[1]);
+            if (ok && t < nt[1]) do_pv(t, 1, true);
           }
         }
       } else {
@@ -327,19 +336,23 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
           for (int t = 0; ok && t < n_loc; ++t) {
             const int st = t % L::STAGES;
             if (t < n) {
-              do_pv(t, g);
-              if (ok) mma_commit(kv_empty(st));
+              do_pv(t, g, true);
             } else {
               // not this query tile's: its arrival for the stage, once per fill
               ok = wait(v_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV);
-              if (ok) mbar_arrive(kv_empty(st));
+              ok = __all_sync(0xffffffffu, ok);
+              if (ok && elect_one()) mbar_arrive(kv_empty(st));
+              __syncwarp();
             }
           }
         }
       }
       // every product this warp issued completes before tensor memory is released
-      mma_commit(fin);
-      mbar_drain_wait(fin, 0, p.status);
+      if (elect_one()) {
+        mma_commit(fin);
+        mbar_drain_wait(fin, 0, p.status);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kHighRegs));
