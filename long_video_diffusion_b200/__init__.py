@@ -544,21 +544,26 @@ def sublayer_planes(work, n_win: int, hidden: int):
 
 # ------------------------------------------------------------------------- D: 4-bit projections
 
-def _same_device(ref: torch.Tensor, *others) -> int:
+def _device_of(ref: torch.Tensor, *others) -> int:
     """The CUDA device index of ref; the other tensors (None left out) have to be there too."""
-    if not ref.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
     dev = ref.get_device()
+    if dev < 0:
+        raise ValueError("tensor must live on a CUDA device")
     for t in others:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors on different devices")
     return dev
 
 
 def _call(fn, where: str, dev: int, stream, *args) -> None:
     """fn(*args, stream) with device `dev` current, on `stream` or dev's current stream."""
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError("stream of another device")
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(dev)   # current_stream() without its Stream object: 1 us
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -583,48 +588,49 @@ def mx4_empty(rows: int, k: int, device=None):
 
 def _mx4(codes: torch.Tensor, scales: torch.Tensor, what: str):
     """(rows, k) of a 4-bit matrix, its buffers checked."""
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2:
         raise ValueError(f"{what}: codes must be uint8 [rows, k / 2] and scales uint8")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    rows, k = codes.shape[0], 2 * codes.shape[1]
-    if scales.numel() < -(-rows // 128) * -(-k // 128) * 512:
-        raise ValueError(f"{what}: scales hold fewer than mx4_scale_bytes({rows}, {k}) bytes")
+    rows, half = codes.shape
+    if scales.numel() < (rows + 127 >> 7) * (half + 63 >> 6) * 512:
+        raise ValueError(f"{what}: scales hold fewer than mx4_scale_bytes({rows}, {2 * half}) bytes")
+    return rows, 2 * half
+
+
+def _mx4_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, what: str):
+    rows, k = _mx4(codes, scales, what)
+    if x.shape != (rows, k) or not x.is_contiguous():
+        raise ValueError(f"{what}: codes [{rows}, {k // 2}] belong to a contiguous [{rows}, {k}], not {tuple(x.shape)}")
     return rows, k
 
 
 def mx4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """x [rows][k] (bf16, f16 or f32) to microscaled 4-bit codes and scales (dp_mx4_quantize);
     codes uint8 [rows][k / 2], scales uint8 of at least mx4_scale_bytes(rows, k)."""
-    dev = _same_device(x, codes, scales)
-    if x.dim() != 2 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous [rows, k]")
-    if _mx4(codes, scales, "mx4_quantize") != tuple(x.shape):
-        raise ValueError("codes must be [rows, k / 2] for x [rows, k]")
-    _call(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, x.data_ptr(), x.shape[0], x.shape[1], _dtype(x),
-          codes.data_ptr(), scales.data_ptr())
+    dev = _device_of(x, codes, scales)
+    rows, k = _mx4_rows(x, codes, scales, "mx4_quantize")
+    _call(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, x.data_ptr(), rows, k, _dtype(x), codes.data_ptr(),
+          scales.data_ptr())
 
 
 def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """The values that codes and scales stand for (dp_mx4_dequantize); y [rows][k] bf16, f16 or f32."""
-    dev = _same_device(y, codes, scales)
-    if y.dim() != 2 or not y.is_contiguous():
-        raise ValueError("y must be a contiguous [rows, k]")
-    if _mx4(codes, scales, "mx4_dequantize") != tuple(y.shape):
-        raise ValueError("y must be [rows, k] for codes [rows, k / 2]")
-    _call(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), y.shape[0],
-          y.shape[1], y.data_ptr(), _dtype(y))
+    dev = _device_of(y, codes, scales)
+    rows, k = _mx4_rows(y, codes, scales, "mx4_dequantize")
+    _call(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, k,
+          y.data_ptr(), _dtype(y))
 
 
 def mx4_linear(a, a_scales, w, w_scales, bias, y, stream=None) -> None:
     """y = a W^T + bias on 4-bit operands (dp_mx4_linear): a [m][k] and w [n][k] as codes and
     scales, bias float [n] or None, y [m][n] bf16, f16 or f32."""
-    dev = _same_device(y, a, a_scales, w, w_scales, bias)
+    dev = _device_of(y, a, a_scales, w, w_scales, bias)
     m, k = _mx4(a, a_scales, "a")
     n, kw = _mx4(w, w_scales, "w")
     if kw != k or y.shape != (m, n) or not y.is_contiguous():
         raise ValueError(f"a [{m}, {k}], w [{n}, {kw}] and a contiguous y {tuple(y.shape)} do not match")
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n,) or not bias.is_contiguous()):
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (n,) or not bias.is_contiguous()):
         raise ValueError("bias must be float32 [n]")
     _call(_lib.dp_mx4_linear, "dp_mx4_linear", dev, stream, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
           w_scales.data_ptr(), None if bias is None else bias.data_ptr(), m, n, k, y.data_ptr(), _dtype(y))
@@ -632,14 +638,14 @@ def mx4_linear(a, a_scales, w, w_scales, bias, y, stream=None) -> None:
 
 # ------------------------------------------------------------------------- E: packed attention
 
-def _pitch(t: torch.Tensor, what: str) -> int:
-    """Elements between rows of t [rows, heads, head_dim], whose rows must be contiguous."""
-    if t.dim() != 3:
-        raise ValueError(f"{what} must be [rows, heads, head_dim]")
-    rows, heads, d = t.shape
-    if (t.stride(2) != 1 and d > 1) or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{what}: a row's heads must be contiguous")
-    return t.stride(0) if rows > 1 else heads * d
+def _pitch(t: torch.Tensor, heads: int, d: int) -> int:
+    """Elements between rows of t [rows, heads, d], whose rows must be contiguous."""
+    if t.is_contiguous():
+        return heads * d
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (heads > 1 and head != d):
+        raise ValueError("a row's heads must be contiguous")
+    return row if t.shape[0] > 1 else heads * d
 
 
 def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
@@ -652,22 +658,26 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
     behind the other too).  Its queries are its last rows: causal, query t sees the keys
     j <= k_lens[i] - q_lens[i] + t.  lse: float32 [q_rows, heads] or None.  A query that sees no
     key gets out = 0 and lse = -inf; rows behind the last sequence are left as they are."""
-    dev = _same_device(q, k, v, out, lse)
+    dev = _device_of(q, k, v, out, lse)
     n = len(q_lens)
     if len(k_lens) != n or (k_starts is not None and len(k_starts) != n):
         raise ValueError("q_lens, k_lens and k_starts differ in length")
-    lq, lk, lv, lo = _pitch(q, "q"), _pitch(k, "k"), _pitch(v, "v"), _pitch(out, "out")
-    if out.shape != q.shape or k.shape != v.shape or q.shape[2] != k.shape[2]:
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v and out must be [rows, heads, head_dim]")
+    (rows, heads, d), (k_rows, kv_heads, dk) = q.shape, k.shape
+    if out.shape != q.shape or v.shape != k.shape or dk != d:
         raise ValueError("shapes of q and out, or of k and v, or their head_dim differ")
-    if k.dtype != q.dtype or v.dtype != q.dtype or out.dtype != q.dtype:
+    lq, lk, lv, lo = _pitch(q, heads, d), _pitch(k, kv_heads, d), _pitch(v, kv_heads, d), _pitch(out, heads, d)
+    dt = q.dtype
+    if k.dtype is not dt or v.dtype is not dt or out.dtype is not dt:
         raise TypeError("q, k, v and out differ in dtype")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [q_rows, heads]")
     arr = _I64 * n
     _call(_lib.dp_packed_attention, "dp_packed_attention", dev, stream, q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
-          lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(), q.shape[0], k.shape[0], arr(*q_lens),
-          arr(*k_lens), None if k_starts is None else arr(*k_starts), n, q.shape[1], k.shape[1], q.shape[2],
-          softmax_scale, CAUSAL if causal else 0, _dtype(q))
+          lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(), rows, k_rows, arr(*q_lens), arr(*k_lens),
+          None if k_starts is None else arr(*k_starts), n, heads, kv_heads, d, softmax_scale, CAUSAL if causal else 0,
+          _dtype(q))
 
 
 def profile_begin(max_steps: int) -> None:
