@@ -20,18 +20,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive elements as fp32.
+// The eight elements of a thread's row as fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-    const T* h = reinterpret_cast<const T*>(&x);
+__device__ __forceinline__ void unpack8(const uint4* raw, float (&f)[8]) {
+  const T* h = reinterpret_cast<const T*>(raw);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(h[e]);
-  }
+  for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(h[e]);
 }
 
 // Four e2m1 pairs, element 0 in the lowest bits.
@@ -91,43 +85,89 @@ __device__ __forceinline__ Unit unit_of_thread(int tiles) {
   return u;
 }
 
+// The larger of two pairs of 16-bit magnitudes, given by their bits: those order like the values,
+// infinities and NaN last.
+__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restrict__ x, uint32_t* __restrict__ codes,
                                                                 uint32_t* __restrict__ scales, int64_t n_rows, int k,
                                                                 int tiles) {
+  constexpr bool kWide = sizeof(T) == 4;
   const Unit u = unit_of_thread(tiles);
   const int sub = threadIdx.x & 15;
-  float f[4][8];
+  uint4 raw[4][kWide ? 2 : 1];
   bool in[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     in[j] = u.row0 + 32 * j < n_rows && u.col < k;
+    const uint4* src = reinterpret_cast<const uint4*>(x + (u.row0 + 32 * j) * k + u.col);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[j][e] = 0.0f;
-    if (in[j]) load8(x + (u.row0 + 32 * j) * k + u.col, f[j]);
+    for (int h = 0; h < (kWide ? 2 : 1); ++h) raw[j][h] = in[j] ? __ldcs(src + h) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t word[4];
+  // each row's largest magnitude in its block of 32 (four threads), as fp32 bits
+  uint32_t top[4];
+  if constexpr (kWide) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m = max(m, max(raw[j][h].x & 0x7fffffffu, raw[j][h].y & 0x7fffffffu));
+        m = max(m, max(raw[j][h].z & 0x7fffffffu, raw[j][h].w & 0x7fffffffu));
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      top[j] = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    }
+  } else {
+    // two rows' 16-bit magnitudes in one word
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      uint32_t m[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4 v = raw[j + r][0];
+        m[r] = umax2(umax2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), umax2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+      }
+      uint32_t both = umax2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+      both = umax2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+      both = umax2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&both));
+        top[j] = __float_as_uint(t.x);
+        top[j + 1] = __float_as_uint(t.y);
+      } else {
+        top[j] = both << 16;
+        top[j + 1] = both & 0xffff0000u;
+      }
+    }
+  }
+  uint32_t mine = 0;  // this block's four scale bytes, row j's at byte j
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[j][e]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t ex = m >> 23;
+    const uint32_t ex = (top[j] >> 23) & 255u;
     const uint32_t byte = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-    const float inv = __uint_as_float((ex == 255u ? 127u : 254u - byte) << 23);
+    mine |= byte << (8 * j);
     if (in[j]) {
+      const float inv = __uint_as_float((ex == 255u ? 127u : 254u - byte) << 23);
+      float f[8];
+      unpack8<T>(raw[j], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[j][e] *= inv;
-      codes[((u.row0 + 32 * j) * k + u.col) >> 3] = pack_e2m1x8(f[j]);
+      for (int e = 0; e < 8; ++e) f[e] *= inv;
+      codes[((u.row0 + 32 * j) * k + u.col) >> 3] = pack_e2m1x8(f);
     }
-    uint32_t w = byte << (8 * (sub >> 2));
-    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    word[j] = w | __shfl_xor_sync(0xffffffffu, w, 8);
   }
-  if (sub == 0)
-    *reinterpret_cast<uint4*>(scales + (mx4_scale_at(u.row0, u.tile * 4, tiles) >> 2)) = make_uint4(word[0], word[1], word[2], word[3]);
+  // 4 x 4 bytes turned between the four blocks' threads: block b's thread gets row b's word
+  const int b = sub >> 2;
+  uint32_t o = __shfl_xor_sync(0xffffffffu, mine, 4);
+  mine = (b & 1) ? __byte_perm(mine, o, 0x3715) : __byte_perm(mine, o, 0x6240);
+  o = __shfl_xor_sync(0xffffffffu, mine, 8);
+  mine = (b & 2) ? __byte_perm(mine, o, 0x3276) : __byte_perm(mine, o, 0x5410);
+  if ((sub & 3) == 0) scales[(mx4_scale_at(u.row0, u.tile * 4, tiles) >> 2) + b] = mine;
 }
 
 template <typename T>
