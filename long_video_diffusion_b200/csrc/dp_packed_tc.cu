@@ -40,9 +40,6 @@ namespace dp {
 namespace {
 
 constexpr int BM = 128;
-constexpr int NQ = 2;            // query tiles per block
-constexpr int kTileRows = NQ * BM;
-constexpr int kTmemCols = 512;
 constexpr int kMaxSplits = 8;    // portable cluster size
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -56,22 +53,25 @@ constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 constexpr float kMinX = -125.0f;
 constexpr uint32_t kPolyMask = 0x1111u;  // column pairs of each 16 that use it
 
-template <int HD>
+template <int HD, int NQ>
 struct Lay {
-  static constexpr int BN = HD == 64 ? 128 : 64;
+  static constexpr int CTAS = NQ == 1 ? 2 : 1;  // per SM
+  static constexpr int kTileRows = NQ * BM;
+  static constexpr int kTmemCols = NQ == 1 ? 256 : 512;
+  static constexpr int BN = HD == 64 && NQ == 2 ? 128 : 64;
   static constexpr int W_PROD = 4 * NQ;
   static constexpr int W_ISS = W_PROD + 1;
   static constexpr int kThreads = 32 * (W_PROD + 4);
-  static constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
-  static constexpr int kLowRegs = 72, kHighRegs = 216;
+  static constexpr int kLaunchRegs = (65536 / (CTAS * kThreads)) & ~7;
+  static constexpr int kLowRegs = 72, kHighRegs = NQ == 1 ? 184 : 216;
   static_assert(NQ * 128 * kHighRegs + 128 * kLowRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
   static constexpr int KCH = HD / 64;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = NQ == 1 && HD == 128 ? 2 : 4;
   static constexpr int Q_CHUNK = BM * 128;
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int Q_BYTES = BM * HD * 2;
   static constexpr int KV_BYTES = BN * HD * 2;
-  static constexpr bool S_PER_TILE = HD > BN;  // the issuers' split (see above)
+  static constexpr bool S_PER_TILE = NQ == 2 && HD > BN;  // the issuers' split (see above)
   static constexpr int COL_S = HD >= BN ? NQ * HD : 0;
   static constexpr int COL_P = COL_S + NQ * BN;
   static constexpr int COL_O = HD >= BN ? 0 : COL_P + NQ * (BN / 2);
@@ -89,7 +89,7 @@ struct Lay {
   static constexpr int O_PITCH = HD + 4;
   static constexpr int OFF_ML = kTileRows * O_PITCH * 4;
   static_assert(OFF_ML + kTileRows * 8 <= OFF_BAR, "the join's rows fit before the barriers");
-  static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+  static_assert(CTAS * (ALLOC + 1024) <= 228 * 1024, "shared memory budget");
 };
 
 struct PackedParams {
@@ -132,12 +132,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-template <int HD, bool F16, int N>
-__global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
+template <int HD, bool F16, int N, int NQ>
+__global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const PackedParams p, const __grid_constant__ PackedSeqs<N> seqs) {
-  using L = Lay<HD>;
+  using L = Lay<HD, NQ>;
   constexpr int BN = L::BN;
+  constexpr int kTileRows = L::kTileRows, kTmemCols = L::kTmemCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -161,11 +162,11 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     const int seen = end > row0 + g * BM ? min(k_len, keys_seen((end - 1) / p.group, q_len, k_len, p.causal)) : 0;
     nt[g] = (seen + BN - 1) / BN;
   }
-  const int per = (max(nt[0], nt[1]) + p.splits - 1) / p.splits;
+  const int per = (max(nt[0], nt[NQ - 1]) + p.splits - 1) / p.splits;
   const int t_begin = rank * per;
 #pragma unroll
   for (int g = 0; g < NQ; ++g) nt[g] = max(0, min(nt[g] - t_begin, per));
-  const int n_loc = max(nt[0], nt[1]);
+  const int n_loc = max(nt[0], nt[NQ - 1]);
   // the last tile of the part ends behind the sequence
   const int tail_rows = n_loc > 0 ? k_len - (t_begin + n_loc - 1) * BN : BN;
   const bool tail = tail_rows < BN;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
       const uint64_t dq0 = sdesc_sw128(sb + L::OFF_Q, 16, 1024);
       const uint64_t dk0 = sdesc_sw128(sb + L::OFF_K, 16, 1024);
       const uint64_t dv0 = sdesc_sw128(sb + L::OFF_V, L::KV_CHUNK, 1024);
-      bool ok = wait(q_full(0), 0, DEV_ERR_TIMEOUT_Q) && wait(q_full(1), 0, DEV_ERR_TIMEOUT_Q);
+      bool ok = wait(q_full(0), 0, DEV_ERR_TIMEOUT_Q) && wait(q_full(NQ - 1), 0, DEV_ERR_TIMEOUT_Q);
       ok = __all_sync(0xffffffffu, ok);
       // S_g of tile t, once K_t is there and S_g of tile t - 1 is in the softmax's registers
       auto do_s = [&](int t, int g) {
@@ -316,23 +317,23 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
       const int iw = warp - L::W_ISS;
       if constexpr (L::S_PER_TILE) {
         if (iw < NQ) {
-          const int n = iw == 0 ? nt[0] : nt[1];
+          const int n = iw == 0 ? nt[0] : nt[NQ - 1];
           for (int t = 0; ok && t < n; ++t) do_s(t, iw);
         } else {
           for (int t = 0; ok && t < n_loc; ++t) {
-            if (t < nt[0]) do_pv(t, 0, t >= nt[1]);
-            if (ok && t < nt[1]) do_pv(t, 1, true);
+            if (t < nt[0]) do_pv(t, 0, t >= nt[NQ - 1]);
+            if (ok && t < nt[NQ - 1]) do_pv(t, 1, true);
           }
         }
       } else {
         if (iw == 0) {
           for (int t = 0; ok && t < n_loc; ++t) {
             if (t < nt[0]) do_s(t, 0);
-            if (ok && t < nt[1]) do_s(t, 1);
+            if (NQ == 2 && ok && t < nt[NQ - 1]) do_s(t, 1);
           }
-        } else {
+        } else if (iw <= NQ) {
           const int g = iw - 1;
-          const int n = g == 0 ? nt[0] : nt[1];
+          const int n = g == 0 ? nt[0] : nt[NQ - 1];
           for (int t = 0; ok && t < n_loc; ++t) {
             const int st = t % L::STAGES;
             if (t < n) {
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     // ------------------------------------------------------------ softmax
     const int g = warp >> 2;
     const int t = threadIdx.x & 127;
-    const int my_nt = g == 0 ? nt[0] : nt[1];
+    const int my_nt = g == 0 ? nt[0] : nt[NQ - 1];
     const int row = row0 + g * BM + t;
     const bool row_ok = row < rows;
     const int tok = row_ok ? row / p.group : 0;
@@ -367,14 +368,26 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     // keys that this row sees (a row behind the last one needs no mask: nothing of it is stored)
     const int lim = row_ok ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : INT_MAX;
 
+    // A row is HD / 8 pieces of 16 bytes.  Rows are read and written by HD / 8 neighbouring lanes
+    // each (a lane per row would touch 32 lines with every access: 3.7 us to load 256 rows of 128
+    // and 2.5 us to store them), and turned in the Q tile's shared memory.
+    constexpr int LPR = HD / 8;    // lanes per row
+    constexpr int RPI = 32 / LPR;  // rows per access of a warp
+    uint8_t* sq = smem + L::OFF_Q + g * L::Q_BYTES;
+    auto piece = [&](int r, int c) {  // 16-byte piece c of row r of the tile
+      return reinterpret_cast<uint4*>(sq + (c >> 3) * L::Q_CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    };
+    const int64_t q_row = (first_q + static_cast<int64_t>(tok));
     {
-      uint8_t* sq = smem + L::OFF_Q + g * L::Q_BYTES;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (first_q + static_cast<int64_t>(tok)) * p.ld_q + head * HD);
+      const int64_t at = row_ok ? q_row * p.ld_q + head * HD : -1;
+      uint4 x[32 / RPI];
 #pragma unroll
-      for (int c = 0; c < HD / 8; ++c) {
-        const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sq + (c >> 3) * L::Q_CHUNK + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = x;
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, i * RPI + lane / LPR);
+        x[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + from) + lane % LPR) : make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int i = 0; i < 32 / RPI; ++i) *piece((warp & 3) * 32 + i * RPI + lane / LPR, lane % LPR) = x[i];
       fence_proxy_async_smem();
       mbar_arrive(q_full(g));
     }
@@ -541,8 +554,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     const bool sees = lim > 0;
     if (p.splits == 1) {
       if (ok && live) {
-        const float inv_l = 1.0f / l_sum;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + (first_q + static_cast<int64_t>(tok)) * p.ld_out + head * HD);
+        const float inv_l = sees ? 1.0f / l_sum : 0.0f;
 #pragma unroll
         for (int c0 = 0; c0 < HD; c0 += 32) {
           uint32_t r[32];
@@ -550,25 +562,28 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
             tmem_ld32(o_col + c0, r);
             tmem_wait_ld();
           }
-          if (row_ok) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<F16>(__uint_as_float(r[c * 8 + 2 * e]) * inv_l, __uint_as_float(r[c * 8 + 2 * e + 1]) * inv_l);
-              dst[c0 / 8 + c] = sees ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack2<F16>(__uint_as_float(r[c * 8 + 2 * e]) * inv_l, __uint_as_float(r[c * 8 + 2 * e + 1]) * inv_l);
+            *piece(t, c0 / 8 + c) = sees ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
           }
         }
-        if (p.lse && row_ok)
-          p.lse[(first_q + static_cast<int64_t>(tok)) * p.n_heads + head] =
-              sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+        if (p.lse && row_ok) p.lse[q_row * p.n_heads + head] = sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+        __syncwarp();
+        const int64_t at = row_ok ? q_row * p.ld_out + head * HD : -1;
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int64_t to = __shfl_sync(0xffffffffu, at, i * RPI + lane / LPR);
+          if (to >= 0) reinterpret_cast<uint4*>(p.out + to)[lane % LPR] = *piece((warp & 3) * 32 + i * RPI + lane / LPR, lane % LPR);
+        }
       }
     } else {
-      // the part's result where the join finds it; Q, K and V have been read once both
-      // warpgroups are here
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // the part's result where the join finds it; Q, K and V have been read once all the softmax
+      // warps are here
+      asm volatile("bar.sync 1, %0;" ::"n"(NQ * 128) : "memory");
       if (ok && live) {
         float* od = reinterpret_cast<float*>(smem) + (g * BM + t) * L::O_PITCH;
         if (my_nt > 0) {
@@ -641,25 +656,25 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
 // Blocks per cluster: one, unless the block with the most key tiles would run longer than an even
 // share of all tiles over the SMs; each part keeps at least four tiles, about the cost of a
 // block's start and join.
-int choose_splits(const PackedArgs& a, int bn, int sms) {
+int choose_splits(const PackedArgs& a, int tile_rows, int bn, int slots) {
   const int group = a.n_heads / a.n_kv_heads;
   int64_t most = 0, total = 0;
   for (int i = 0; i < a.n_seqs; ++i) {
-    const int64_t row_tiles = (static_cast<int64_t>(a.q_len[i]) * group + kTileRows - 1) / kTileRows;
+    const int64_t row_tiles = (static_cast<int64_t>(a.q_len[i]) * group + tile_rows - 1) / tile_rows;
     const int64_t key_tiles = (static_cast<int64_t>(a.k_len[i]) + bn - 1) / bn;
     most = key_tiles > most ? key_tiles : most;
     total += row_tiles * key_tiles * a.n_kv_heads;
   }
   int splits = 1;
-  while (splits < kMaxSplits && most > 4 * 2 * splits - 1 && most * sms > total * splits) splits *= 2;
+  while (splits < kMaxSplits && most > 4 * 2 * splits - 1 && most * slots > total * splits) splits *= 2;
   return splits;
 }
 
-template <int HD, bool F16, int N>
+template <int HD, bool F16, int N, int NQ>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
-  using L = Lay<HD>;
+  using L = Lay<HD, NQ>;
   PackedSeqs<N> seqs;
-  const int64_t tiles = plan_packed(a, kTileRows, seqs);
+  const int64_t tiles = plan_packed(a, L::kTileRows, seqs);
   int64_t key_rows = 0;
   for (int i = 0; i < a.n_seqs; ++i) {
     const int64_t end = static_cast<int64_t>(a.first_k[i]) + a.k_len[i];
@@ -679,7 +694,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  auto kernel = packed_attn_tc_kernel<HD, F16, N>;
+  auto kernel = packed_attn_tc_kernel<HD, F16, N, NQ>;
   static std::atomic<bool> attr_set[64];
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
@@ -699,7 +714,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.n_heads = a.n_heads;
   p.n_kv = a.n_kv_heads;
   p.group = a.n_heads / a.n_kv_heads;
-  p.splits = choose_splits(a, L::BN, sms);
+  p.splits = choose_splits(a, L::kTileRows, L::BN, L::CTAS * sms);
   p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.status = a.status;
@@ -720,9 +735,18 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int HD, bool F16, int N>
+cudaError_t launch_seqs(const PackedArgs& a, cudaStream_t s) {
+#ifdef FORCE_NQ
+  return launch_n<HD, F16, N, FORCE_NQ>(a, s);
+#else
+  return launch_n<HD, F16, N, 2>(a, s);
+#endif
+}
+
 template <int HD, bool F16>
 cudaError_t launch_hd(const PackedArgs& a, cudaStream_t s) {
-  return a.n_seqs <= kFewSeqs ? launch_n<HD, F16, kFewSeqs>(a, s) : launch_n<HD, F16, DP_MAX_SEQS>(a, s);
+  return a.n_seqs <= kFewSeqs ? launch_seqs<HD, F16, kFewSeqs>(a, s) : launch_seqs<HD, F16, DP_MAX_SEQS>(a, s);
 }
 
 }  // namespace
