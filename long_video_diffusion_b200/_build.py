@@ -19,7 +19,7 @@ LIB_NAME = "libdp_b200.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["dp_api.cu", "dp_attn_tc.cu", "dp_attn_f32.cu", "dp_gemm.cu", "dp_modulate.cu", "dp_noalloc.cu",
-           "dp_mx4.cu", "dp_mx4_gemm.cu", "dp_packed.cu", "dp_packed_tc.cu"]
+           "dp_mx4.cu", "dp_mx4_gemm.cu", "dp_packed.cu", "dp_packed_tc.cu", "dp_packed_few.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "-shared",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

@@ -165,7 +165,7 @@ struct Mx4Args {
 };
 cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s);
 
-// Attention over packed sequences (dp_packed_f32.cu, dp_packed_tc.cu).  Only sequences with query rows;
+// Attention over packed sequences (dp_packed.cu, dp_packed_tc.cu, dp_packed_few.cu).  Only sequences with query rows;
 // first_q[i] is sequence i's first query row.
 struct PackedArgs {
   const void* q;
@@ -188,7 +188,6 @@ struct PackedArgs {
   uint32_t* status;
 };
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s);
-cudaError_t launch_packed_tc(const PackedArgs& a, cudaStream_t s);  // bf16, f16
 
 // The driver's tensor-map encoder, NULL if it has none (defined in dp_attn_tc.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

@@ -44,6 +44,25 @@ int64_t plan_packed(const PackedArgs& a, int rows, int32_t* n, int32_t* tile0, i
   return tiles;
 }
 
+bool encode_packed_kv(const PackedArgs& a, int box_rows, bool f16, CUtensorMap* tk, CUtensorMap* tv) {
+  int64_t rows = 0;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int64_t end = static_cast<int64_t>(a.first_k[i]) + a.k_len[i];
+    if (a.k_len[i] > 0 && end > rows) rows = end;
+  }
+  const int cols = a.n_kv_heads * a.head_dim;
+  // with no keys at all nothing is loaded: q's first row will do for the maps
+  if (!rows) return encode_tmap_16_pitch(tk, a.q, 1, cols, a.ld_q, box_rows, f16) && encode_tmap_16_pitch(tv, a.q, 1, cols, a.ld_q, box_rows, f16);
+  return encode_tmap_16_pitch(tk, a.k, rows, cols, a.ld_k, box_rows, f16) && encode_tmap_16_pitch(tv, a.v, rows, cols, a.ld_v, box_rows, f16);
+}
+
+cudaError_t device_and_sms(int* dev, int* sms) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+}
+
 namespace {
 
 constexpr int kWarps = 8;
@@ -218,7 +237,11 @@ cudaError_t launch_t(const PackedArgs& a, cudaStream_t st) {
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s) {
   if (a.n_seqs < 1 || a.n_seqs > DP_MAX_SEQS || (a.head_dim != 64 && a.head_dim != 128)) return cudaErrorInvalidValue;
   if (a.dt == DP_F32) return launch_t<float>(a, s);
-  return launch_packed_tc(a, s);
+  // few rows: bound by reading the keys, which the kernel for few rows does at twice the rate
+  const int group = a.n_heads / a.n_kv_heads;
+  bool few = true;
+  for (int i = 0; i < a.n_seqs; ++i) few = few && static_cast<int64_t>(a.q_len[i]) * group <= kFewRows;
+  return few ? launch_packed_few(a, s) : launch_packed_tc(a, s);
 }
 
 }  // namespace dp

@@ -51,4 +51,88 @@ int64_t plan_packed(const PackedArgs& a, int rows, PackedSeqs<N>& s) {
 
 constexpr int kFewSeqs = 32;  // launches of up to this many sequences carry a small argument (0.7 KB, not 20)
 
+// An item is a tile of rows under one k/v head, k/v heads fastest.  The keys of the first
+// n_cut items are cut into as many parts as a cluster has blocks; the clusters behind theirs
+// take one whole item per block.
+constexpr int kMaxCluster = 8;  // portable cluster size
+
+struct Cut {
+  int cluster;
+  int64_t items;
+};
+
+struct ItemPart {
+  int item, rank, parts;
+};
+
+__device__ __forceinline__ ItemPart item_part(int cluster, int n_cut) {
+  const int c = blockIdx.x / cluster, r = blockIdx.x % cluster;
+  if (c < n_cut) return ItemPart{c, r, cluster};
+  return ItemPart{n_cut + (c - n_cut) * cluster + r, 0, 1};
+}
+
+// The cluster size, and with it which sequences' keys are cut, that promises the earliest end:
+// an even share of all key tiles, with `overhead` tiles for each block's start and end, over
+// `slots` blocks at a time, or the longest part, whichever is later.
+template <int N>
+Cut choose_cut(const PackedArgs& a, const PackedSeqs<N>& s, int bn, int slots, int overhead) {
+  auto key_tiles = [&](int i) { return (static_cast<int64_t>(s.k_len[i]) + bn - 1) / bn; };
+  int64_t total = 0;
+  for (int i = 0; i < s.n; ++i) {
+    // causal: a sequence's row tiles see from k_len - q_len to k_len keys
+    const int64_t fewest = !a.causal ? s.k_len[i] : s.k_len[i] > s.q_len[i] ? s.k_len[i] - s.q_len[i] : 0;
+    total += (s.tile0[i + 1] - s.tile0[i]) * (((fewest + s.k_len[i]) / 2 + bn - 1) / bn);
+  }
+  total *= a.n_kv_heads;
+  const int64_t items = static_cast<int64_t>(s.tile0[s.n]) * a.n_kv_heads;
+  const int64_t most = key_tiles(0);
+  Cut best = {1, 0};
+  int64_t best_end = -1;
+  for (int c = 1; c <= kMaxCluster && (c == 1 || most >= 2 * c); c *= 2) {
+    const int64_t part = (most + c - 1) / c;
+    Cut now = {c, 0};
+    if (c > 1)
+      for (int i = 0; i < s.n && key_tiles(i) > part; ++i) now.items = static_cast<int64_t>(s.tile0[i + 1]) * a.n_kv_heads;
+    const int64_t share = (total + overhead * (items + now.items * (c - 1))) / slots;
+    const int64_t end = share > part + overhead ? share : part + overhead;
+    if (best_end < 0 || end < best_end) {
+      best = now;
+      best_end = end;
+    }
+  }
+  return best;
+}
+
+// Tensor maps of k and v with boxes of `box_rows` keys by 64 columns.
+bool encode_packed_kv(const PackedArgs& a, int box_rows, bool f16, CUtensorMap* tk, CUtensorMap* tv);
+
+cudaError_t device_and_sms(int* dev, int* sms);  // the current device (ordinal < 64) and its SMs
+
+// One block per item or part of one.
+template <typename K, typename... A>
+cudaError_t launch_items(K kernel, const Cut& cut, int64_t items, int threads, int smem, cudaStream_t s, const A&... args) {
+  const int64_t grid = (cut.items + (items - cut.items + cut.cluster - 1) / cut.cluster) * cut.cluster;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cut.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cut.cluster > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The kernels for bf16 and f16: few rows (at most kFewRows of a sequence under one k/v head,
+// dp_packed_few.cu) or many (dp_packed_tc.cu).
+constexpr int kFewRows = 16;
+constexpr int kFewOverhead = 6;  // key tiles that a block's start and end cost in dp_packed_few.cu
+cudaError_t launch_packed_few(const PackedArgs& a, cudaStream_t s);
+cudaError_t launch_packed_tc(const PackedArgs& a, cudaStream_t s);
+
 }  // namespace dp

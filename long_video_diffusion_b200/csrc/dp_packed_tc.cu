@@ -19,7 +19,8 @@
 // Few rows and many keys (single tokens over a cache): the keys are cut into as many parts as a
 // thread-block cluster has blocks, each block keeps its part's O, maximum and sum, and at the
 // end the blocks join them through distributed shared memory, in a fixed order, with no
-// workspace and no second launch.
+// workspace and no second launch.  Only the sequences with many keys are cut (they come first);
+// the blocks of the clusters behind them take one whole item each.
 //
 // A tile of keys that ends behind its sequence holds other rows: their scores are masked, and
 // the producer warp writes zeros over their V rows before the product reads them (0 * NaN).
@@ -40,7 +41,6 @@ namespace dp {
 namespace {
 
 constexpr int BM = 128;
-constexpr int kMaxSplits = 8;    // portable cluster size
 constexpr float kRescaleLog2 = 8.0f;
 
 // 2^x on the FMA pipe for some columns (the MUFU unit gives 16 exponentials per clock and SM, as
@@ -71,6 +71,7 @@ struct Lay {
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int Q_BYTES = BM * HD * 2;
   static constexpr int KV_BYTES = BN * HD * 2;
+  static constexpr int kOverhead = NQ == 1 ? 7 : 5;  // key tiles that a block's start and end cost
   static constexpr bool S_PER_TILE = NQ == 2 && HD > BN;  // the issuers' split (see above)
   static constexpr int COL_S = HD >= BN ? NQ * HD : 0;
   static constexpr int COL_P = COL_S + NQ * BN;
@@ -98,7 +99,9 @@ struct PackedParams {
   float* lse;
   int64_t ld_q, ld_out;
   int32_t n_heads, n_kv, group;
-  int32_t splits;  // blocks per cluster
+  int32_t cluster;  // blocks per cluster
+  int32_t n_cut;    // items whose keys a cluster's blocks share; n_items: all
+  int32_t n_items;
   int32_t causal;
   float scale_log2;
   uint32_t* status;
@@ -146,8 +149,9 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   const int lane = threadIdx.x & 31;
 
   // this block's rows and its part of their keys
-  const int rank = blockIdx.x % p.splits;
-  const int item = blockIdx.x / p.splits;
+  const ItemPart ip = item_part(p.cluster, p.n_cut);
+  const int item = ip.item, rank = ip.rank, splits = ip.parts;
+  if (item >= p.n_items) return;  // behind the last item: its cluster never joins
   const int kv = item % p.n_kv;
   const int tile = item / p.n_kv;
   const int seq = seq_of_tile(seqs, tile);
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     const int seen = end > row0 + g * BM ? min(k_len, keys_seen((end - 1) / p.group, q_len, k_len, p.causal)) : 0;
     nt[g] = (seen + BN - 1) / BN;
   }
-  const int per = (max(nt[0], nt[NQ - 1]) + p.splits - 1) / p.splits;
+  const int per = (max(nt[0], nt[NQ - 1]) + splits - 1) / splits;
   const int t_begin = rank * per;
 #pragma unroll
   for (int g = 0; g < NQ; ++g) nt[g] = max(0, min(nt[g] - t_begin, per));
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       tc_fence_after();
     }
     const bool sees = lim > 0;
-    if (p.splits == 1) {
+    if (splits == 1) {
       if (ok && live) {
         const float inv_l = sees ? 1.0f / l_sum : 0.0f;
 #pragma unroll
@@ -609,20 +613,20 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (p.splits > 1) {
+  if (splits > 1) {
     cluster_sync();
     // block `rank` joins the rows r = rank, rank + splits, ...: four columns per thread
     const int n_rows = min(kTileRows, rows - row0);
-    const int n_mine = (n_rows - rank + p.splits - 1) / p.splits;
+    const int n_mine = (n_rows - rank + splits - 1) / splits;
     for (int i = threadIdx.x; i < n_mine * (HD / 4); i += L::kThreads) {
-      const int r = rank + (i / (HD / 4)) * p.splits;
+      const int r = rank + (i / (HD / 4)) * splits;
       const int c = (i % (HD / 4)) * 4;
-      float2 ml[kMaxSplits];
-      float4 o[kMaxSplits];
+      float2 ml[kMaxCluster];
+      float4 o[kMaxCluster];
       float top = -INFINITY;
 #pragma unroll
-      for (int s = 0; s < kMaxSplits; ++s)
-        if (s < p.splits) {
+      for (int s = 0; s < kMaxCluster; ++s)
+        if (s < splits) {
           ml[s] = ld_peer2(peer_smem(sb + L::OFF_ML + r * 8, s));
           o[s] = ld_peer4(peer_smem(sb + (r * L::O_PITCH + c) * 4, s));
           top = fmaxf(top, ml[s].x);
@@ -630,8 +634,8 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       float4 a = make_float4(0, 0, 0, 0);
       float l = 0.0f;
 #pragma unroll
-      for (int s = 0; s < kMaxSplits; ++s)
-        if (s < p.splits && ml[s].x != -INFINITY) {
+      for (int s = 0; s < kMaxCluster; ++s)
+        if (s < splits && ml[s].x != -INFINITY) {
           const float w = ex2_approx(ml[s].x - top);
           l = fmaf(w, ml[s].y, l);
           a.x = fmaf(w, o[s].x, a.x);
@@ -653,46 +657,16 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   }
 }
 
-// Blocks per cluster: one, unless the block with the most key tiles would run longer than an even
-// share of all tiles over the SMs; each part keeps at least four tiles, about the cost of a
-// block's start and join.
-int choose_splits(const PackedArgs& a, int tile_rows, int bn, int slots) {
-  const int group = a.n_heads / a.n_kv_heads;
-  int64_t most = 0, total = 0;
-  for (int i = 0; i < a.n_seqs; ++i) {
-    const int64_t row_tiles = (static_cast<int64_t>(a.q_len[i]) * group + tile_rows - 1) / tile_rows;
-    const int64_t key_tiles = (static_cast<int64_t>(a.k_len[i]) + bn - 1) / bn;
-    most = key_tiles > most ? key_tiles : most;
-    total += row_tiles * key_tiles * a.n_kv_heads;
-  }
-  int splits = 1;
-  while (splits < kMaxSplits && most > 4 * 2 * splits - 1 && most * slots > total * splits) splits *= 2;
-  return splits;
-}
-
 template <int HD, bool F16, int N, int NQ>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   using L = Lay<HD, NQ>;
   PackedSeqs<N> seqs;
   const int64_t tiles = plan_packed(a, L::kTileRows, seqs);
-  int64_t key_rows = 0;
-  for (int i = 0; i < a.n_seqs; ++i) {
-    const int64_t end = static_cast<int64_t>(a.first_k[i]) + a.k_len[i];
-    if (a.k_len[i] > 0 && end > key_rows) key_rows = end;
-  }
+  if (tiles < 0 || tiles * a.n_kv_heads > INT_MAX) return cudaErrorInvalidValue;
   CUtensorMap tk, tv;
-  // with no keys at all nothing is loaded: any rows will do for the maps
-  const void* k = key_rows ? a.k : a.q;
-  const void* v = key_rows ? a.v : a.q;
-  const int cols = a.n_kv_heads * HD;
-  if (!encode_tmap_16_pitch(&tk, k, key_rows ? key_rows : 1, cols, key_rows ? a.ld_k : a.ld_q, L::BN, F16) ||
-      !encode_tmap_16_pitch(&tv, v, key_rows ? key_rows : 1, cols, key_rows ? a.ld_v : a.ld_q, L::BN, F16))
-    return cudaErrorInvalidValue;
+  if (!encode_packed_kv(a, L::BN, F16, &tk, &tv)) return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   auto kernel = packed_attn_tc_kernel<HD, F16, N, NQ>;
   static std::atomic<bool> attr_set[64];
@@ -714,25 +688,15 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.n_heads = a.n_heads;
   p.n_kv = a.n_kv_heads;
   p.group = a.n_heads / a.n_kv_heads;
-  p.splits = choose_splits(a, L::kTileRows, L::BN, L::CTAS * sms);
+  const Cut cut = choose_cut(a, seqs, L::BN, L::CTAS * sms, L::kOverhead);
+  p.cluster = cut.cluster;
+  p.n_cut = static_cast<int32_t>(cut.items);
   p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.status = a.status;
-  const int64_t grid = tiles * a.n_kv_heads * p.splits;
-  if (tiles < 0 || grid > INT_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::ALLOC;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.splits > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p, seqs);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const int64_t items = tiles * a.n_kv_heads;
+  p.n_items = static_cast<int32_t>(items);
+  return launch_items(kernel, cut, items, L::kThreads, L::ALLOC, s, tk, tv, p, seqs);
 }
 
 template <int HD, bool F16, int N>
