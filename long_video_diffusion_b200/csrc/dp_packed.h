@@ -20,6 +20,21 @@ struct PackedSeqs {
   int32_t k_len[N];
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery): with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (umulhi(n, m) + n) >> s.  The divisors of a launch are
+// known to the host, and a block's start is a chain of these: five divisions took it 0.5 us.
+struct FastDiv {
+  uint32_t m, s;
+  __device__ __forceinline__ int div(int n) const { return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s); }
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {0, 0};
+  while ((1ull << f.s) < d) ++f.s;
+  f.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+  return f;
+}
+
 // The sequence of tile t: the last i with tile0[i] <= t.
 template <int N>
 __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N>& s, int t) {
@@ -57,18 +72,20 @@ constexpr int kFewSeqs = 32;  // launches of up to this many sequences carry a s
 constexpr int kMaxCluster = 8;  // portable cluster size
 
 struct Cut {
-  int cluster;
+  int cluster;  // a power of two
   int64_t items;
+  int log_cluster() const { return cluster == 8 ? 3 : cluster == 4 ? 2 : cluster == 2 ? 1 : 0; }
 };
 
 struct ItemPart {
-  int item, rank, parts;
+  int item, rank, log_parts;
 };
 
-__device__ __forceinline__ ItemPart item_part(int cluster, int n_cut) {
-  const int c = blockIdx.x / cluster, r = blockIdx.x % cluster;
-  if (c < n_cut) return ItemPart{c, r, cluster};
-  return ItemPart{n_cut + (c - n_cut) * cluster + r, 0, 1};
+// log_cluster: log2 of the cluster size.  The parts' number is a power of two too.
+__device__ __forceinline__ ItemPart item_part(int log_cluster, int n_cut) {
+  const int c = blockIdx.x >> log_cluster, r = blockIdx.x & ((1 << log_cluster) - 1);
+  if (c < n_cut) return ItemPart{c, r, log_cluster};
+  return ItemPart{n_cut + ((c - n_cut) << log_cluster) + r, 0, 0};
 }
 
 // The cluster size, and with it which sequences' keys are cut, that promises the earliest end:

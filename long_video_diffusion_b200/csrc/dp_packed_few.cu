@@ -53,7 +53,8 @@ struct FewParams {
   float* lse;
   int64_t ld_q, ld_out;
   int32_t n_heads, n_kv, group;
-  int32_t cluster, n_cut, n_items;
+  FastDiv by_kv, by_group;
+  int32_t log_cluster, n_cut, n_items;
   int32_t causal;
   float scale_log2;
   uint32_t* status;
@@ -100,12 +101,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const ItemPart ip = item_part(p.cluster, p.n_cut);
+  const ItemPart ip = item_part(p.log_cluster, p.n_cut);
   if (ip.item >= p.n_items) return;  // behind the last item: its cluster never joins
+  const int parts = 1 << ip.log_parts;
   auto full = [&](int s) { return sb + L::OFF_BAR + 8u * s; };
   auto empty = [&](int s) { return sb + L::OFF_BAR + 8u * (L::STAGES + s); };
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
-  if (threadIdx.x == 0) {
+  if (warp == kWarps && lane == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int s = 0; s < L::STAGES; ++s) {
@@ -116,35 +118,42 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_mbar_init();
   }
   // the cluster's blocks have started before one writes into another
-  if (ip.parts > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  if (parts > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
-  const int kv = ip.item % p.n_kv;
-  const int seq = ip.item / p.n_kv;  // one tile of rows per sequence
+  const int seq = p.by_kv.div(ip.item);  // one tile of rows per sequence
+  const int kv = ip.item - seq * p.n_kv;
   const int q_len = seqs.q_len[seq], k_len = seqs.k_len[seq];
   const int first_q = seqs.first_q[seq], first_k = seqs.first_k[seq];
   const int rows = q_len * p.group;
   const int seen = min(k_len, keys_seen(q_len - 1, q_len, k_len, p.causal));
   const int tiles = (seen + kKeys - 1) / kKeys;
-  const int per = (tiles + ip.parts - 1) / ip.parts;
+  const int per = (tiles + parts - 1) >> ip.log_parts;
   const int t_begin = ip.rank * per;
   const int n_loc = max(0, min(tiles - t_begin, per));
+
+  // Key tile t of the part into its stage.
+  auto load_tile = [&](int t) {
+    const int s = t % L::STAGES;
+    mbar_arrive_expect_tx(full(s), L::STAGE);
+    const int row = first_k + (t_begin + t) * kKeys;
+#pragma unroll
+    for (int c = 0; c < L::CHUNKS; ++c) {
+      tma_load_2d(sb + s * L::STAGE + c * L::CHUNK, &tm_k, kv * HD + c * 64, row, full(s));
+      tma_load_2d(sb + s * L::STAGE + (L::CHUNKS + c) * L::CHUNK, &tm_v, kv * HD + c * 64, row, full(s));
+    }
+  };
+  // the first stages' loads, before the others are up
+  int issued = 0;
+  if (warp == kWarps && lane == 0)
+    for (; issued < min(n_loc, L::STAGES); ++issued) load_tile(issued);
   __syncthreads();
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int issued = 0;
-      for (int t = 0; t < n_loc; ++t) {
-        const int s = t % L::STAGES;
-        if (t >= L::STAGES && !mbar_wait(empty(s), (t / L::STAGES - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
-        mbar_arrive_expect_tx(full(s), L::STAGE);
-        const int row = first_k + (t_begin + t) * kKeys;
-#pragma unroll
-        for (int c = 0; c < L::CHUNKS; ++c) {
-          tma_load_2d(sb + s * L::STAGE + c * L::CHUNK, &tm_k, kv * HD + c * 64, row, full(s));
-          tma_load_2d(sb + s * L::STAGE + (L::CHUNKS + c) * L::CHUNK, &tm_v, kv * HD + c * 64, row, full(s));
-        }
-        issued = t + 1;
+      for (; issued < n_loc; ++issued) {
+        if (!mbar_wait(empty(issued % L::STAGES), (issued / L::STAGES - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
+        load_tile(issued);
       }
       for (int t = max(0, issued - L::STAGES); t < issued; ++t) mbar_drain_wait(full(t % L::STAGES), (t / L::STAGES) & 1, p.status);
     }
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = lane / 4 + 8 * h;
-      const int tok = row / p.group;
+      const int tok = p.by_group.div(row);
       lim[h] = row < rows ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : 0;
       const uint16_t* src = p.q + (first_q + static_cast<int64_t>(tok)) * p.ld_q + (kv * p.group + row - tok * p.group) * HD + pair;
 #pragma unroll
@@ -266,11 +275,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncthreads();
   // ------------------------------------------------------------ the warps' results joined
-  if (ip.parts > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (parts > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   const float2* wml = reinterpret_cast<const float2*>(smem + L::OFF_WML);
-  const int width = HD / ip.parts;  // columns that each of the cluster's blocks joins
+  const int width = HD >> ip.log_parts;  // columns that each of the cluster's blocks joins
   auto finish = [&](int row, int c, float4 a, float top, float l) {
-    const int tok = row / p.group;
+    const int tok = p.by_group.div(row);
     const int head = kv * p.group + row - tok * p.group;
     const bool sees = top != -INFINITY;
     const float inv = sees ? 1.0f / l : 0.0f;
@@ -299,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       a.z = fmaf(g, x.z, a.z);
       a.w = fmaf(g, x.w, a.w);
     }
-    if (ip.parts == 1) {
+    if (parts == 1) {
       finish(row, c, a, top, l);
     } else {
       const int to = c / width;
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  if (ip.parts > 1) {
+  if (parts > 1) {
     // ---------------------------------------------------------- the parts joined, this block's columns
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     const float2* pml = reinterpret_cast<const float2*>(smem + L::OFF_ML);
@@ -319,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = threadIdx.x; i < rows * (width / 4); i += kThreads) {
       const int row = i / (width / 4), c = (i % (width / 4)) * 4;
       float top = -INFINITY, l = 0.0f;
-      for (int s = 0; s < ip.parts; ++s) top = fmaxf(top, pml[s * kRows + row].x);
+      for (int s = 0; s < parts; ++s) top = fmaxf(top, pml[s * kRows + row].x);
       float4 a = make_float4(0, 0, 0, 0);
-      for (int s = 0; s < ip.parts; ++s) {
+      for (int s = 0; s < parts; ++s) {
         const float2 ml = pml[s * kRows + row];
         const float g = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - top);
         const float4 x = *reinterpret_cast<const float4*>(join + (s * kRows + row) * width + c);
@@ -365,7 +374,9 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.n_heads = a.n_heads;
   p.n_kv = a.n_kv_heads;
   p.group = a.n_heads / a.n_kv_heads;
-  p.cluster = cut.cluster;
+  p.by_kv = fast_div(p.n_kv);
+  p.by_group = fast_div(p.group);
+  p.log_cluster = cut.log_cluster();
   p.n_cut = static_cast<int32_t>(cut.items);
   p.n_items = static_cast<int32_t>(items);
   p.causal = a.causal;

@@ -99,7 +99,8 @@ struct PackedParams {
   float* lse;
   int64_t ld_q, ld_out;
   int32_t n_heads, n_kv, group;
-  int32_t cluster;  // blocks per cluster
+  FastDiv by_kv, by_group;
+  int32_t log_cluster;  // of the blocks per cluster
   int32_t n_cut;    // items whose keys a cluster's blocks share; n_items: all
   int32_t n_items;
   int32_t causal;
@@ -148,32 +149,9 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // this block's rows and its part of their keys
-  const ItemPart ip = item_part(p.cluster, p.n_cut);
-  const int item = ip.item, rank = ip.rank, splits = ip.parts;
+  const ItemPart ip = item_part(p.log_cluster, p.n_cut);
+  const int item = ip.item, rank = ip.rank, splits = 1 << ip.log_parts;
   if (item >= p.n_items) return;  // behind the last item: its cluster never joins
-  const int kv = item % p.n_kv;
-  const int tile = item / p.n_kv;
-  const int seq = seq_of_tile(seqs, tile);
-  const int q_len = seqs.q_len[seq], k_len = seqs.k_len[seq];
-  const int first_q = seqs.first_q[seq], first_k = seqs.first_k[seq];
-  const int rows = q_len * p.group;
-  const int row0 = (seqs.tile0[seq + 1] - 1 - tile) * kTileRows;
-  int nt[NQ];  // key tiles of each query tile, then those of this block's part
-#pragma unroll
-  for (int g = 0; g < NQ; ++g) {
-    const int end = min(rows, row0 + (g + 1) * BM);  // behind the query tile's last row
-    const int seen = end > row0 + g * BM ? min(k_len, keys_seen((end - 1) / p.group, q_len, k_len, p.causal)) : 0;
-    nt[g] = (seen + BN - 1) / BN;
-  }
-  const int per = (max(nt[0], nt[NQ - 1]) + splits - 1) / splits;
-  const int t_begin = rank * per;
-#pragma unroll
-  for (int g = 0; g < NQ; ++g) nt[g] = max(0, min(nt[g] - t_begin, per));
-  const int n_loc = max(nt[0], nt[NQ - 1]);
-  // the last tile of the part ends behind the sequence
-  const int tail_rows = n_loc > 0 ? k_len - (t_begin + n_loc - 1) * BN : BN;
-  const bool tail = tail_rows < BN;
 
   const uint32_t bar0 = sb + L::OFF_BAR;
   auto k_full = [&](int s) { return bar0 + 8u * s; };
@@ -189,7 +167,9 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
-  if (threadIdx.x == 0) {
+  if (warp == L::W_PROD && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
     for (int s = 0; s < L::STAGES; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(v_full(s), 1);
@@ -211,10 +191,47 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == L::W_PROD && lane == 0) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+  // this block's rows and its part of their keys
+  const int tile = p.by_kv.div(item);
+  const int kv = item - tile * p.n_kv;
+  const int seq = seq_of_tile(seqs, tile);
+  const int q_len = seqs.q_len[seq], k_len = seqs.k_len[seq];
+  const int first_q = seqs.first_q[seq], first_k = seqs.first_k[seq];
+  const int rows = q_len * p.group;
+  const int row0 = (seqs.tile0[seq + 1] - 1 - tile) * kTileRows;
+  int nt[NQ];  // key tiles of each query tile, then those of this block's part
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) {
+    const int end = min(rows, row0 + (g + 1) * BM);  // behind the query tile's last row
+    const int seen = end > row0 + g * BM ? min(k_len, keys_seen(p.by_group.div(end - 1), q_len, k_len, p.causal)) : 0;
+    nt[g] = (seen + BN - 1) / BN;
   }
+  const int per = (max(nt[0], nt[NQ - 1]) + splits - 1) >> ip.log_parts;
+  const int t_begin = rank * per;
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) nt[g] = max(0, min(nt[g] - t_begin, per));
+  const int n_loc = max(nt[0], nt[NQ - 1]);
+  // the last tile of the part ends behind the sequence
+  const int tail_rows = n_loc > 0 ? k_len - (t_begin + n_loc - 1) * BN : BN;
+  const bool tail = tail_rows < BN;
+
+  // Key tile j of the part into its stage.
+  auto load_tile = [&](int j) {
+    const int st = j % L::STAGES;
+    const int row = first_k + (t_begin + j) * BN;
+    mbar_arrive_expect_tx(k_full(st), L::KV_BYTES);
+#pragma unroll
+    for (int c = 0; c < L::KCH; ++c)
+      tma_load_2d(sb + L::OFF_K + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_k, kv * HD + c * 64, row, k_full(st));
+    mbar_arrive_expect_tx(v_full(st), L::KV_BYTES);
+#pragma unroll
+    for (int c = 0; c < L::KCH; ++c)
+      tma_load_2d(sb + L::OFF_V + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_v, kv * HD + c * 64, row, v_full(st));
+  };
+  // the first stages' loads, before the others are up
+  int issued = 0;
+  if (warp == L::W_PROD && lane == 0)
+    for (; issued < min(n_loc, L::STAGES); ++issued) load_tile(issued);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -224,22 +241,10 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLowRegs));
     if (warp == L::W_PROD) {
       // ------------------------------------------------------------ TMA producer
-      int issued = 0;
       if (lane == 0) {
-        for (int j = 0; j < n_loc; ++j) {
-          const int st = j % L::STAGES;
-          const int use = j / L::STAGES;
-          if (use > 0 && !mbar_wait(kv_empty(st), (use - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
-          const int row = first_k + (t_begin + j) * BN;
-          mbar_arrive_expect_tx(k_full(st), L::KV_BYTES);
-#pragma unroll
-          for (int c = 0; c < L::KCH; ++c)
-            tma_load_2d(sb + L::OFF_K + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_k, kv * HD + c * 64, row, k_full(st));
-          mbar_arrive_expect_tx(v_full(st), L::KV_BYTES);
-#pragma unroll
-          for (int c = 0; c < L::KCH; ++c)
-            tma_load_2d(sb + L::OFF_V + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_v, kv * HD + c * 64, row, v_full(st));
-          issued = j + 1;
+        for (; issued < n_loc; ++issued) {
+          if (!mbar_wait(kv_empty(issued % L::STAGES), (issued / L::STAGES - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
+          load_tile(issued);
         }
       }
       issued = __shfl_sync(0xffffffffu, issued, 0);
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     const int my_nt = g == 0 ? nt[0] : nt[NQ - 1];
     const int row = row0 + g * BM + t;
     const bool row_ok = row < rows;
-    const int tok = row_ok ? row / p.group : 0;
+    const int tok = row_ok ? p.by_group.div(row) : 0;
     const int head = kv * p.group + (row_ok ? row - tok * p.group : 0);
     // keys that this row sees (a row behind the last one needs no mask: nothing of it is stored)
     const int lim = row_ok ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : INT_MAX;
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     cluster_sync();
     // block `rank` joins the rows r = rank, rank + splits, ...: four columns per thread
     const int n_rows = min(kTileRows, rows - row0);
-    const int n_mine = (n_rows - rank + splits - 1) / splits;
+    const int n_mine = (n_rows - rank + splits - 1) >> ip.log_parts;
     for (int i = threadIdx.x; i < n_mine * (HD / 4); i += L::kThreads) {
       const int r = rank + (i / (HD / 4)) * splits;
       const int c = (i % (HD / 4)) * 4;
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
           a.w = fmaf(w, o[s].w, a.w);
         }
       const int row = row0 + r;
-      const int tok = row / p.group;
+      const int tok = p.by_group.div(row);
       const int head = kv * p.group + row - tok * p.group;
       const bool sees = top != -INFINITY;
       const float inv = sees ? 1.0f / l : 0.0f;
@@ -689,7 +694,9 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.n_kv = a.n_kv_heads;
   p.group = a.n_heads / a.n_kv_heads;
   const Cut cut = choose_cut(a, seqs, L::BN, L::CTAS * sms, L::kOverhead);
-  p.cluster = cut.cluster;
+  p.by_kv = fast_div(p.n_kv);
+  p.by_group = fast_div(p.group);
+  p.log_cluster = cut.log_cluster();
   p.n_cut = static_cast<int32_t>(cut.items);
   p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
