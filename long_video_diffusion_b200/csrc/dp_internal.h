@@ -197,5 +197,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 bool encode_tmap_16(void* tmap, const void* base, int64_t rows, int hidden, int box_rows, bool f16);
 // The same with rows `pitch` elements apart.
 bool encode_tmap_16_pitch(void* tmap, const void* base, int64_t rows, int hidden, int64_t pitch, int box_rows, bool f16);
+// [rows][n_heads][head_dim] with rows `pitch` elements apart, {64 columns, box_heads, box_rows} boxes.
+bool encode_tmap_16_heads(void* tmap, const void* base, int64_t rows, int n_heads, int head_dim, int64_t pitch, int box_heads,
+                          int box_rows, bool f16);
 
 }  // namespace dp

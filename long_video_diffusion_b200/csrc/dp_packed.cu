@@ -19,14 +19,13 @@
 
 namespace dp {
 
-int64_t plan_packed(const PackedArgs& a, int rows, int32_t* n, int32_t* tile0, int32_t* first_q, int32_t* q_len,
+int64_t plan_packed(const PackedArgs& a, int64_t per_token, int rows, int32_t* n, int32_t* tile0, int32_t* first_q, int32_t* q_len,
                     int32_t* first_k, int32_t* k_len) {
   int32_t order[DP_MAX_SEQS];
   for (int i = 0; i < a.n_seqs; ++i) order[i] = i;
   std::sort(order, order + a.n_seqs, [&](int32_t x, int32_t y) {
     return a.k_len[x] != a.k_len[y] ? a.k_len[x] > a.k_len[y] : x < y;
   });
-  const int64_t group = a.n_heads / a.n_kv_heads;
   int64_t tiles = 0;
   *n = a.n_seqs;
   for (int i = 0; i < a.n_seqs; ++i) {
@@ -36,8 +35,8 @@ int64_t plan_packed(const PackedArgs& a, int rows, int32_t* n, int32_t* tile0, i
     q_len[i] = a.q_len[o];
     first_k[i] = a.first_k[o];
     k_len[i] = a.k_len[o];
-    if (a.q_len[o] * group > INT_MAX) return -1;
-    tiles += (a.q_len[o] * group + rows - 1) / rows;
+    if (a.q_len[o] * per_token > INT_MAX) return -1;
+    tiles += (a.q_len[o] * per_token + rows - 1) / rows;
     if (tiles > INT_MAX) return -1;
   }
   tile0[a.n_seqs] = static_cast<int32_t>(tiles);
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __res
 template <typename T, int HD, int N>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   PackedSeqs<N> s;
-  const int64_t tiles = plan_packed(a, kRows, s);
+  const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, s);
   if (tiles < 0 || a.n_kv_heads > 65535) return cudaErrorInvalidValue;
   constexpr int bytes = (kKeys * (HD + 4) + kKeys * HD + kRows * HD) * 4;
   int dev = 0;

@@ -7,7 +7,7 @@ namespace dp {
 
 // The query rows of a sequence under one k/v head are its tokens' rows of the `group` query
 // heads that share it: row r is token r / group, head r % group of the group.  They are cut
-// into tiles of a kernel's row count; tile0[i] is sequence i's first tile.  The host puts the
+// into a kernel's tiles; tile0[i] is sequence i's first tile.  The host puts the
 // sequences with the most keys first, and a sequence's last tile (causal: the one with the
 // most keys) is its first, so that the longest work starts first.
 template <int N>
@@ -55,13 +55,14 @@ __host__ __device__ __forceinline__ int keys_seen(int tok, int q_len, int k_len,
   return n < 0 ? 0 : n;
 }
 
-// Fills s for tiles of `rows` rows; returns the number of tiles, or -1 if it passes 2^31 - 1.
-int64_t plan_packed(const PackedArgs& a, int rows, int32_t* n, int32_t* tile0, int32_t* first_q, int32_t* q_len,
+// Fills s for tiles that hold `rows` of the q_len * per_token rows of a sequence; returns the number
+// of tiles, or -1 if it passes 2^31 - 1.
+int64_t plan_packed(const PackedArgs& a, int64_t per_token, int rows, int32_t* n, int32_t* tile0, int32_t* first_q, int32_t* q_len,
                     int32_t* first_k, int32_t* k_len);
 
 template <int N>
-int64_t plan_packed(const PackedArgs& a, int rows, PackedSeqs<N>& s) {
-  return plan_packed(a, rows, &s.n, s.tile0, s.first_q, s.q_len, s.first_k, s.k_len);
+int64_t plan_packed(const PackedArgs& a, int64_t per_token, int rows, PackedSeqs<N>& s) {
+  return plan_packed(a, per_token, rows, &s.n, s.tile0, s.first_q, s.q_len, s.first_k, s.k_len);
 }
 
 constexpr int kFewSeqs = 32;  // launches of up to this many sequences carry a small argument (0.7 KB, not 20)
@@ -90,18 +91,18 @@ __device__ __forceinline__ ItemPart item_part(int log_cluster, int n_cut) {
 
 // The cluster size, and with it which sequences' keys are cut, that promises the earliest end:
 // an even share of all key tiles, with `overhead` tiles for each block's start and end, over
-// `slots` blocks at a time, or the longest part, whichever is later.
+// `slots` blocks at a time, or the longest part, whichever is later.  per_tile: items per row tile.
 template <int N>
-Cut choose_cut(const PackedArgs& a, const PackedSeqs<N>& s, int bn, int slots, int overhead) {
+Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, int slots, int overhead) {
   auto key_tiles = [&](int i) { return (static_cast<int64_t>(s.k_len[i]) + bn - 1) / bn; };
   int64_t total = 0;
   for (int i = 0; i < s.n; ++i) {
     // causal: a sequence's row tiles see from k_len - q_len to k_len keys
-    const int64_t fewest = !a.causal ? s.k_len[i] : s.k_len[i] > s.q_len[i] ? s.k_len[i] - s.q_len[i] : 0;
+    const int64_t fewest = !causal ? s.k_len[i] : s.k_len[i] > s.q_len[i] ? s.k_len[i] - s.q_len[i] : 0;
     total += (s.tile0[i + 1] - s.tile0[i]) * (((fewest + s.k_len[i]) / 2 + bn - 1) / bn);
   }
-  total *= a.n_kv_heads;
-  const int64_t items = static_cast<int64_t>(s.tile0[s.n]) * a.n_kv_heads;
+  total *= per_tile;
+  const int64_t items = static_cast<int64_t>(s.tile0[s.n]) * per_tile;
   const int64_t most = key_tiles(0);
   Cut best = {1, 0};
   int64_t best_end = -1;
@@ -109,7 +110,7 @@ Cut choose_cut(const PackedArgs& a, const PackedSeqs<N>& s, int bn, int slots, i
     const int64_t part = (most + c - 1) / c;
     Cut now = {c, 0};
     if (c > 1)
-      for (int i = 0; i < s.n && key_tiles(i) > part; ++i) now.items = static_cast<int64_t>(s.tile0[i + 1]) * a.n_kv_heads;
+      for (int i = 0; i < s.n && key_tiles(i) > part; ++i) now.items = static_cast<int64_t>(s.tile0[i + 1]) * per_tile;
     const int64_t share = (total + overhead * (items + now.items * (c - 1))) / slots;
     const int64_t end = share > part + overhead ? share : part + overhead;
     if (best_end < 0 || end < best_end) {

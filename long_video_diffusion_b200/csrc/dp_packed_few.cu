@@ -349,7 +349,7 @@ template <int HD, bool F16, int N>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   using L = Few<HD>;
   PackedSeqs<N> seqs;
-  const int64_t tiles = plan_packed(a, kRows, seqs);
+  const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, seqs);
   if (tiles != a.n_seqs || tiles * a.n_kv_heads > INT_MAX) return cudaErrorInvalidValue;
   CUtensorMap tk, tv;
   if (!encode_packed_kv(a, kKeys, F16, &tk, &tv)) return cudaErrorInvalidValue;
@@ -364,7 +364,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
     attr_set[dev].store(true, std::memory_order_release);
   }
   const int64_t items = tiles * a.n_kv_heads;
-  const Cut cut = choose_cut(a, seqs, kKeys, 2 * sms, kFewOverhead);
+  const Cut cut = choose_cut(a.causal, seqs, a.n_kv_heads, kKeys, 2 * sms, kFewOverhead);
   FewParams p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.out = static_cast<uint16_t*>(a.out);

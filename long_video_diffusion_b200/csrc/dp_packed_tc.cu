@@ -1,9 +1,11 @@
 // Attention over packed sequences on the sm_100a tensor cores (bf16 or f16; the fp32 form is in
 // dp_packed.cu, which also states the formulas).
 //
-// One block = one k/v head's two tiles of 128 query rows of one sequence; a row is a (token,
-// head of the group) pair (dp_packed.h), so that a tile's keys are read once for all the heads
-// that share them and a single token fills as many rows as its group has heads.  Keys go by in
+// One block = one or two query tiles of one sequence under one k/v head; a tile is as many whole
+// tokens as their rows, one for each head of the group, fit in 128 (groups of more than 128 heads
+// are cut), so that its keys are read once for all the heads that share them, and one TMA box
+// {64 columns, heads, tokens} brings 64 columns of it.  (256 threads with 16 loads each took 5 us
+// to bring 256 rows of 128 under load.)  Keys go by in
 // tiles of BN rows (128 at head_dim 64, 64 at head_dim 128) up to the last one that a row of the
 // tile sees; only tiles that the mask cuts pay for it (warp-uniform test).
 //   warps 0-3  softmax of query tile 0, one thread per row
@@ -94,12 +96,13 @@ struct Lay {
 };
 
 struct PackedParams {
-  const uint16_t* q;
   uint16_t* out;
   float* lse;
-  int64_t ld_q, ld_out;
-  int32_t n_heads, n_kv, group;
-  FastDiv by_kv, by_group;
+  int64_t ld_out;
+  int32_t n_heads, n_kv, group;  // n_kv: k/v heads times the cuts of a group
+  int32_t cuts, cut_heads;       // of a group of more than 128 heads (else 1, group)
+  int32_t tokens;                // of a query tile
+  FastDiv by_kv, by_cut_heads;
   int32_t log_cluster;  // of the blocks per cluster
   int32_t n_cut;    // items whose keys a cluster's blocks share; n_items: all
   int32_t n_items;
@@ -138,8 +141,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 template <int HD, bool F16, int N, int NQ>
 __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
-    packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const PackedParams p, const __grid_constant__ PackedSeqs<N> seqs) {
+    packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PackedParams p, const __grid_constant__ PackedSeqs<N> seqs) {
   using L = Lay<HD, NQ>;
   constexpr int BN = L::BN;
   constexpr int kTileRows = L::kTileRows, kTmemCols = L::kTmemCols;
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
   if (warp == L::W_PROD && lane == 0) {
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int s = 0; s < L::STAGES; ++s) {
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       mbar_init(kv_empty(s), L::S_PER_TILE ? 1 : NQ);
     }
     for (int g = 0; g < NQ; ++g) {
-      mbar_init(q_full(g), 128);
+      mbar_init(q_full(g), 1);
       mbar_init(s_full(g), 1);
       mbar_init(s_free(g), 128);
       mbar_init(p_full(g), 128);
@@ -193,17 +197,19 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   }
   // this block's rows and its part of their keys
   const int tile = p.by_kv.div(item);
-  const int kv = item - tile * p.n_kv;
+  const int kvc = item - tile * p.n_kv;
+  const int kv = p.cuts == 1 ? kvc : kvc / p.cuts;
+  const int head0 = kv * p.group + (kvc - kv * p.cuts) * p.cut_heads;
+  const int heads = min(p.cut_heads, (kv + 1) * p.group - head0);
   const int seq = seq_of_tile(seqs, tile);
   const int q_len = seqs.q_len[seq], k_len = seqs.k_len[seq];
   const int first_q = seqs.first_q[seq], first_k = seqs.first_k[seq];
-  const int rows = q_len * p.group;
-  const int row0 = (seqs.tile0[seq + 1] - 1 - tile) * kTileRows;
+  const int tok0 = (seqs.tile0[seq + 1] - 1 - tile) * (NQ * p.tokens);  // the first query tile's first token
   int nt[NQ];  // key tiles of each query tile, then those of this block's part
 #pragma unroll
   for (int g = 0; g < NQ; ++g) {
-    const int end = min(rows, row0 + (g + 1) * BM);  // behind the query tile's last row
-    const int seen = end > row0 + g * BM ? min(k_len, keys_seen(p.by_group.div(end - 1), q_len, k_len, p.causal)) : 0;
+    const int end = min(q_len, tok0 + (g + 1) * p.tokens);  // behind the query tile's last token
+    const int seen = end > tok0 + g * p.tokens ? min(k_len, keys_seen(end - 1, q_len, k_len, p.causal)) : 0;
     nt[g] = (seen + BN - 1) / BN;
   }
   const int per = (max(nt[0], nt[NQ - 1]) + splits - 1) >> ip.log_parts;
@@ -228,10 +234,19 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     for (int c = 0; c < L::KCH; ++c)
       tma_load_2d(sb + L::OFF_V + st * L::KV_BYTES + c * L::KV_CHUNK, &tm_v, kv * HD + c * 64, row, v_full(st));
   };
-  // the first stages' loads, before the others are up
+  // the query tiles' and the first stages' loads, before the other warps are up
   int issued = 0;
-  if (warp == L::W_PROD && lane == 0)
+  if (warp == L::W_PROD && lane == 0) {
+#pragma unroll
+    for (int g = 0; g < NQ; ++g)
+      if (nt[g] > 0) {
+        mbar_arrive_expect_tx(q_full(g), L::KCH * 128 * p.cut_heads * p.tokens);
+#pragma unroll
+        for (int c = 0; c < L::KCH; ++c)
+          tma_load_3d(sb + L::OFF_Q + g * L::Q_BYTES + c * L::Q_CHUNK, &tm_q, c * 64, head0, first_q + tok0 + g * p.tokens, q_full(g));
+      }
     for (; issued < min(n_loc, L::STAGES); ++issued) load_tile(issued);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -263,6 +278,9 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       }
       if (lane == 0) {
         // every copy this block issued lands before its shared memory is released
+#pragma unroll
+        for (int g = 0; g < NQ; ++g)
+          if (nt[g] > 0) mbar_drain_wait(q_full(g), 0, p.status);
         const int first = issued > L::STAGES ? issued - L::STAGES : 0;
         for (int j = first; j < issued; ++j) {
           mbar_drain_wait(k_full(j % L::STAGES), (j / L::STAGES) & 1, p.status);
@@ -281,12 +299,11 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       const uint64_t dq0 = sdesc_sw128(sb + L::OFF_Q, 16, 1024);
       const uint64_t dk0 = sdesc_sw128(sb + L::OFF_K, 16, 1024);
       const uint64_t dv0 = sdesc_sw128(sb + L::OFF_V, L::KV_CHUNK, 1024);
-      bool ok = wait(q_full(0), 0, DEV_ERR_TIMEOUT_Q) && wait(q_full(NQ - 1), 0, DEV_ERR_TIMEOUT_Q);
-      ok = __all_sync(0xffffffffu, ok);
+      bool ok = true;
       // S_g of tile t, once K_t is there and S_g of tile t - 1 is in the softmax's registers
       auto do_s = [&](int t, int g) {
         const int st = t % L::STAGES;
-        ok = (t == 0 || wait(s_free(g), (t - 1) & 1, DEV_ERR_TIMEOUT_S)) &&
+        ok = (t == 0 ? wait(q_full(g), 0, DEV_ERR_TIMEOUT_Q) : wait(s_free(g), (t - 1) & 1, DEV_ERR_TIMEOUT_S)) &&
              wait(k_full(st), (t / L::STAGES) & 1, DEV_ERR_TIMEOUT_KV);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
@@ -370,36 +387,26 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     const int g = warp >> 2;
     const int t = threadIdx.x & 127;
     const int my_nt = g == 0 ? nt[0] : nt[NQ - 1];
-    const int row = row0 + g * BM + t;
-    const bool row_ok = row < rows;
-    const int tok = row_ok ? p.by_group.div(row) : 0;
-    const int head = kv * p.group + (row_ok ? row - tok * p.group : 0);
-    // keys that this row sees (a row behind the last one needs no mask: nothing of it is stored)
-    const int lim = row_ok ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : INT_MAX;
-
-    // A row is HD / 8 pieces of 16 bytes.  Rows are read and written by HD / 8 neighbouring lanes
-    // each (a lane per row would touch 32 lines with every access: 3.7 us to load 256 rows of 128
-    // and 2.5 us to store them), and turned in the Q tile's shared memory.
-    constexpr int LPR = HD / 8;    // lanes per row
-    constexpr int RPI = 32 / LPR;  // rows per access of a warp
+    // row r of the tile: a token and a head of the group (or of its cut), if they exist
+    auto row_of = [&](int r, int& tok, int& head) {
+      const int of_tok = p.by_cut_heads.div(r);
+      tok = tok0 + g * p.tokens + of_tok;
+      head = head0 + r - of_tok * p.cut_heads;
+      return of_tok < p.tokens && tok < q_len && head < head0 + heads;
+    };
+    // keys that this thread's row sees (a row that does not exist needs no mask: nothing of it is stored)
+    int lim;
+    bool live;
+    {
+      int tok, head;
+      const bool row_ok = row_of(t, tok, head);
+      lim = row_ok ? min(k_len, keys_seen(tok, q_len, k_len, p.causal)) : INT_MAX;
+      live = __any_sync(0xffffffffu, row_ok);
+    }
     uint8_t* sq = smem + L::OFF_Q + g * L::Q_BYTES;
     auto piece = [&](int r, int c) {  // 16-byte piece c of row r of the tile
       return reinterpret_cast<uint4*>(sq + (c >> 3) * L::Q_CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     };
-    const int64_t q_row = (first_q + static_cast<int64_t>(tok));
-    {
-      const int64_t at = row_ok ? q_row * p.ld_q + head * HD : -1;
-      uint4 x[32 / RPI];
-#pragma unroll
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int64_t from = __shfl_sync(0xffffffffu, at, i * RPI + lane / LPR);
-        x[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + from) + lane % LPR) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 32 / RPI; ++i) *piece((warp & 3) * 32 + i * RPI + lane / LPR, lane % LPR) = x[i];
-      fence_proxy_async_smem();
-      mbar_arrive(q_full(g));
-    }
 
     const uint32_t trow = tmem + ((static_cast<uint32_t>(warp & 3) * 32u) << 16);
     const uint32_t s_col = trow + L::COL_S + g * BN;
@@ -408,7 +415,6 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
     constexpr int NCH = BN / 32;
     constexpr int NG = BN / 16;
     const uint64_t sl2 = f32x2(p.scale_log2, p.scale_log2);
-    const bool live = __any_sync(0xffffffffu, row_ok);
     // tiles of this part that every row of the warp sees whole
     const int n_whole = __reduce_min_sync(0xffffffffu, lim) / BN - t_begin;
     float m_ref = -INFINITY;
@@ -561,6 +567,11 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
       tc_fence_after();
     }
     const bool sees = lim > 0;
+    // (worked out again: registers are short over the tiles)
+    int again = t, tok, head;
+    asm volatile("" : "+r"(again));
+    const bool row_ok = row_of(again, tok, head);
+    const int64_t q_row = first_q + static_cast<int64_t>(tok);
     if (splits == 1) {
       if (ok && live) {
         const float inv_l = sees ? 1.0f / l_sum : 0.0f;
@@ -581,6 +592,29 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
           }
         }
         if (p.lse && row_ok) p.lse[q_row * p.n_heads + head] = sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+      }
+      // The tile's output, over its queries, leaves as the queries came; where rows of the box are
+      // not this tile's (the sequence's last tokens, a cut group's last heads) the lanes of a row
+      // store it themselves.
+      if (tok0 + (g + 1) * p.tokens <= q_len && heads == p.cut_heads) {
+        fence_proxy_async_smem();
+        // the warpgroup, whether or not it gave up
+        if (g == 0)
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        else
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+        if (ok && t == 0) {
+#pragma unroll
+          for (int c = 0; c < L::KCH; ++c)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(&tm_o)),
+                         "r"(smem_u32(sq) + c * L::Q_CHUNK), "r"(c * 64), "r"(head0), "r"(first_q + tok0 + g * p.tokens)
+                         : "memory");
+          asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+        }
+      } else if (ok && live) {
+        constexpr int LPR = HD / 8;    // lanes per row
+        constexpr int RPI = 32 / LPR;  // rows per access of a warp
         __syncwarp();
         const int64_t at = row_ok ? q_row * p.ld_out + head * HD : -1;
 #pragma unroll
@@ -621,11 +655,16 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
   if (splits > 1) {
     cluster_sync();
     // block `rank` joins the rows r = rank, rank + splits, ...: four columns per thread
-    const int n_rows = min(kTileRows, rows - row0);
+    const int n_rows = tok0 + p.tokens < q_len ? kTileRows : BM;
     const int n_mine = (n_rows - rank + splits - 1) >> ip.log_parts;
     for (int i = threadIdx.x; i < n_mine * (HD / 4); i += L::kThreads) {
       const int r = rank + (i / (HD / 4)) * splits;
       const int c = (i % (HD / 4)) * 4;
+      const int rg = r & (BM - 1);
+      const int of_tok = p.by_cut_heads.div(rg);
+      const int tok = tok0 + (r / BM) * p.tokens + of_tok;
+      const int head = head0 + rg - of_tok * p.cut_heads;
+      if (of_tok >= p.tokens || tok >= q_len || head >= head0 + heads) continue;
       float2 ml[kMaxCluster];
       float4 o[kMaxCluster];
       float top = -INFINITY;
@@ -648,9 +687,6 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
           a.z = fmaf(w, o[s].z, a.z);
           a.w = fmaf(w, o[s].w, a.w);
         }
-      const int row = row0 + r;
-      const int tok = p.by_group.div(row);
-      const int head = kv * p.group + row - tok * p.group;
       const bool sees = top != -INFINITY;
       const float inv = sees ? 1.0f / l : 0.0f;
       const int64_t at = first_q + static_cast<int64_t>(tok);
@@ -665,11 +701,24 @@ __global__ void __launch_bounds__(Lay<HD, NQ>::kThreads, Lay<HD, NQ>::CTAS)
 template <int HD, bool F16, int N, int NQ>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   using L = Lay<HD, NQ>;
+  const int group = a.n_heads / a.n_kv_heads;
+  PackedParams p;
+  p.cuts = (group + BM - 1) / BM;
+  p.cut_heads = (group + p.cuts - 1) / p.cuts;
+  p.tokens = BM / p.cut_heads;
+  p.n_kv = a.n_kv_heads * p.cuts;
   PackedSeqs<N> seqs;
-  const int64_t tiles = plan_packed(a, L::kTileRows, seqs);
-  if (tiles < 0 || tiles * a.n_kv_heads > INT_MAX) return cudaErrorInvalidValue;
-  CUtensorMap tk, tv;
-  if (!encode_packed_kv(a, L::BN, F16, &tk, &tv)) return cudaErrorInvalidValue;
+  const int64_t tiles = plan_packed(a, 1, NQ * p.tokens, seqs);
+  if (tiles < 0 || tiles * p.n_kv > INT_MAX) return cudaErrorInvalidValue;
+  CUtensorMap tq, tk, tv, to;
+  int64_t q_rows = 0;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int64_t end = static_cast<int64_t>(a.first_q[i]) + a.q_len[i];
+    q_rows = end > q_rows ? end : q_rows;
+  }
+  if (!encode_packed_kv(a, L::BN, F16, &tk, &tv) || !encode_tmap_16_heads(&tq, a.q, q_rows, a.n_heads, HD, a.ld_q, p.cut_heads, p.tokens, F16) ||
+      !encode_tmap_16_heads(&to, a.out, q_rows, a.n_heads, HD, a.ld_out, p.cut_heads, p.tokens, F16))
+    return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
   cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
@@ -684,26 +733,22 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
     if (fa.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;  // setmaxnreg.inc would wait for good
     attr_set[dev].store(true, std::memory_order_release);
   }
-  PackedParams p;
-  p.q = static_cast<const uint16_t*>(a.q);
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
-  p.ld_q = a.ld_q;
   p.ld_out = a.ld_out;
   p.n_heads = a.n_heads;
-  p.n_kv = a.n_kv_heads;
-  p.group = a.n_heads / a.n_kv_heads;
-  const Cut cut = choose_cut(a, seqs, L::BN, L::CTAS * sms, L::kOverhead);
+  p.group = group;
+  const Cut cut = choose_cut(a.causal, seqs, p.n_kv, L::BN, L::CTAS * sms, L::kOverhead);
   p.by_kv = fast_div(p.n_kv);
-  p.by_group = fast_div(p.group);
+  p.by_cut_heads = fast_div(p.cut_heads);
   p.log_cluster = cut.log_cluster();
   p.n_cut = static_cast<int32_t>(cut.items);
   p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.status = a.status;
-  const int64_t items = tiles * a.n_kv_heads;
+  const int64_t items = tiles * p.n_kv;
   p.n_items = static_cast<int32_t>(items);
-  return launch_items(kernel, cut, items, L::kThreads, L::ALLOC, s, tk, tv, p, seqs);
+  return launch_items(kernel, cut, items, L::kThreads, L::ALLOC, s, tq, tk, tv, to, p, seqs);
 }
 
 template <int HD, bool F16, int N>
