@@ -544,31 +544,33 @@ def sublayer_planes(work, n_win: int, hidden: int):
 
 # ------------------------------------------------------------------------- D: 4-bit projections
 
-def _device_of(ref: torch.Tensor, *others) -> int:
-    """The CUDA device index of ref; the other tensors (None left out) have to be there too."""
-    dev = ref.get_device()
-    if dev < 0:
-        raise ValueError("tensor must live on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on different devices")
-    return dev
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream(dev).cuda_stream, 1 us less
+_get_device = torch._C._cuda_getDevice
+_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-def _call(fn, where: str, dev: int, stream, *args) -> None:
+def _device_of(*tensors) -> int:
+    """The CUDA device index of the tensors (None left out), which have to be on one."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) != 1 or -1 in devs:
+        raise ValueError("tensors must live on one CUDA device")
+    return devs.pop()
+
+
+def _launch(fn, where: str, dev: int, stream, args) -> None:
     """fn(*args, stream) with device `dev` current, on `stream` or dev's current stream."""
-    if stream is not None:
-        if stream.device_index != dev:
-            raise ValueError("stream of another device")
+    if stream is None:
+        raw = _raw_stream(dev)
+    elif stream.device_index == dev:
         raw = stream.cuda_stream
     else:
-        raw = torch._C._cuda_getCurrentRawStream(dev)   # current_stream() without its Stream object: 1 us
-    if torch._C._cuda_getDevice() == dev:
+        raise ValueError("stream of another device")
+    if _get_device() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
             st = fn(*args, raw)
-    if st != OK:
+    if st:
         raise DpError(st, where)
 
 
@@ -590,7 +592,7 @@ def _mx4(codes: torch.Tensor, scales: torch.Tensor, what: str):
     """(rows, k) of a 4-bit matrix, its buffers checked."""
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2:
         raise ValueError(f"{what}: codes must be uint8 [rows, k / 2] and scales uint8")
-    if not codes.is_contiguous() or not scales.is_contiguous():
+    if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("tensor must be contiguous")
     rows, half = codes.shape
     if scales.numel() < (rows + 127 >> 7) * (half + 63 >> 6) * 512:
@@ -598,42 +600,46 @@ def _mx4(codes: torch.Tensor, scales: torch.Tensor, what: str):
     return rows, 2 * half
 
 
-def _mx4_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, what: str):
-    rows, k = _mx4(codes, scales, what)
+def _mx4_rows(where: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """(device, rows, k, dtype) of rows x and their 4-bit form, checked."""
+    rows, k = _mx4(codes, scales, where)
     if x.shape != (rows, k) or not x.is_contiguous():
-        raise ValueError(f"{what}: codes [{rows}, {k // 2}] belong to a contiguous [{rows}, {k}], not {tuple(x.shape)}")
-    return rows, k
+        raise ValueError(f"{where}: codes [{rows}, {k // 2}] belong to a contiguous [{rows}, {k}], not {tuple(x.shape)}")
+    return _device_of(x, codes, scales), rows, k, _CODES.get(x.dtype)
 
 
 def mx4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """x [rows][k] (bf16, f16 or f32) to microscaled 4-bit codes and scales (dp_mx4_quantize);
     codes uint8 [rows][k / 2], scales uint8 of at least mx4_scale_bytes(rows, k)."""
-    dev = _device_of(x, codes, scales)
-    rows, k = _mx4_rows(x, codes, scales, "mx4_quantize")
-    _call(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, x.data_ptr(), rows, k, _dtype(x), codes.data_ptr(),
-          scales.data_ptr())
+    dev, rows, k, dt = _mx4_rows("mx4_quantize", x, codes, scales)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    _launch(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, (x.data_ptr(), rows, k, dt, codes.data_ptr(), scales.data_ptr()))
 
 
 def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """The values that codes and scales stand for (dp_mx4_dequantize); y [rows][k] bf16, f16 or f32."""
-    dev = _device_of(y, codes, scales)
-    rows, k = _mx4_rows(y, codes, scales, "mx4_dequantize")
-    _call(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, k,
-          y.data_ptr(), _dtype(y))
+    dev, rows, k, dt = _mx4_rows("mx4_dequantize", y, codes, scales)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {y.dtype}")
+    _launch(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, (codes.data_ptr(), scales.data_ptr(), rows, k, y.data_ptr(), dt))
 
 
 def mx4_linear(a, a_scales, w, w_scales, bias, y, stream=None) -> None:
     """y = a W^T + bias on 4-bit operands (dp_mx4_linear): a [m][k] and w [n][k] as codes and
     scales, bias float [n] or None, y [m][n] bf16, f16 or f32."""
-    dev = _device_of(y, a, a_scales, w, w_scales, bias)
     m, k = _mx4(a, a_scales, "a")
     n, kw = _mx4(w, w_scales, "w")
     if kw != k or y.shape != (m, n) or not y.is_contiguous():
         raise ValueError(f"a [{m}, {k}], w [{n}, {kw}] and a contiguous y {tuple(y.shape)} do not match")
     if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (n,) or not bias.is_contiguous()):
         raise ValueError("bias must be float32 [n]")
-    _call(_lib.dp_mx4_linear, "dp_mx4_linear", dev, stream, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
-          w_scales.data_ptr(), None if bias is None else bias.data_ptr(), m, n, k, y.data_ptr(), _dtype(y))
+    dt = _CODES.get(y.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {y.dtype}")
+    _launch(_lib.dp_mx4_linear, "dp_mx4_linear", _device_of(y, a, a_scales, w, w_scales, bias), stream,
+            (a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
+             m, n, k, y.data_ptr(), dt))
 
 
 # ------------------------------------------------------------------------- E: packed attention
@@ -658,7 +664,6 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
     behind the other too).  Its queries are its last rows: causal, query t sees the keys
     j <= k_lens[i] - q_lens[i] + t.  lse: float32 [q_rows, heads] or None.  A query that sees no
     key gets out = 0 and lse = -inf; rows behind the last sequence are left as they are."""
-    dev = _device_of(q, k, v, out, lse)
     n = len(q_lens)
     if len(k_lens) != n or (k_starts is not None and len(k_starts) != n):
         raise ValueError("q_lens, k_lens and k_starts differ in length")
@@ -673,11 +678,14 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
         raise TypeError("q, k, v and out differ in dtype")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [q_rows, heads]")
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
     arr = _I64 * n
-    _call(_lib.dp_packed_attention, "dp_packed_attention", dev, stream, q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
-          lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(), rows, k_rows, arr(*q_lens), arr(*k_lens),
-          None if k_starts is None else arr(*k_starts), n, heads, kv_heads, d, softmax_scale, CAUSAL if causal else 0,
-          _dtype(q))
+    _launch(_lib.dp_packed_attention, "dp_packed_attention", _device_of(q, k, v, out, lse), stream,
+            (q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(),
+             rows, k_rows, arr(*q_lens), arr(*k_lens), None if k_starts is None else arr(*k_starts), n, heads, kv_heads, d,
+             softmax_scale, CAUSAL if causal else 0, code))
 
 
 def profile_begin(max_steps: int) -> None:

@@ -1,12 +1,11 @@
-// Attention over packed sequences of different lengths, grouped heads, causal or not, on the
-// CUDA cores: every sum in fp32.
+// Attention over packed sequences of different lengths, grouped heads, causal or not: the host's
+// plan for all types, and the fp32 kernel, on the CUDA cores (fp32 inputs ask for more than tf32's
+// 10 bits of mantissa).
 //
 //   out_t,h = sum_j softmax_j(q_t,h . k_j,g * scale) v_j,g,  g = h / group,
 //   j < k_len, causal j <= k_len - q_len + t;  lse_t,h = log sum_j exp(q_t,h . k_j,g * scale)
 //
 // One pass over the keys with a running maximum and sum.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -73,25 +72,14 @@ struct Strides {
   int64_t q, k, v, out;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4*>(p);
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    const T* h = reinterpret_cast<const T*>(&x);
-    return make_float4(static_cast<float>(h[0]), static_cast<float>(h[1]), static_cast<float>(h[2]), static_cast<float>(h[3]));
-  }
-}
-
 // A warp's eight rows against one tile of 32 keys: lane j holds key j's scores, then each lane
 // its columns of the output.
-template <typename T, int HD, int N>
-__global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                                  const T* __restrict__ v, T* __restrict__ out,
-                                                                  float* __restrict__ lse, Strides ld,
-                                                                  const __grid_constant__ PackedSeqs<N> seqs,
-                                                                  int n_heads, int group, float scale, int causal) {
+template <int HD, int N>
+__global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
+                                                                 const float* __restrict__ v, float* __restrict__ out,
+                                                                 float* __restrict__ lse, Strides ld,
+                                                                 const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
+                                                                 int group, float scale, int causal) {
   extern __shared__ float smem[];
   constexpr int KP = HD + 4;  // pitch of a key row: 16-byte reads of 32 rows without conflicts
   float* sk = smem;           // [kKeys][KP]
@@ -111,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __res
     float4 x = make_float4(0, 0, 0, 0);
     if (r < n_rows) {
       const int tok = (row0 + r) / group, h = kv * group + (row0 + r) % group;
-      x = load4(q + (seqs.first_q[s] + static_cast<int64_t>(tok)) * ld.q + h * HD + c);
+      x = *reinterpret_cast<const float4*>(q + (seqs.first_q[s] + static_cast<int64_t>(tok)) * ld.q + h * HD + c);
     }
     float* d = sq + r * HD + c;
     d[0] = x.x * scale, d[1] = x.y * scale, d[2] = x.z * scale, d[3] = x.w * scale;
@@ -134,8 +122,8 @@ __global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __res
       float4 x = make_float4(0, 0, 0, 0), y = x;
       if (j0 + j < k_len) {
         const int64_t row = seqs.first_k[s] + static_cast<int64_t>(j0 + j);
-        x = load4(k + row * ld.k + kv * HD + c);
-        y = load4(v + row * ld.v + kv * HD + c);
+        x = *reinterpret_cast<const float4*>(k + row * ld.k + kv * HD + c);
+        y = *reinterpret_cast<const float4*>(v + row * ld.v + kv * HD + c);
       }
       *reinterpret_cast<float4*>(sk + j * KP + c) = x;
       *reinterpret_cast<float4*>(sv + j * HD + c) = y;
@@ -197,12 +185,12 @@ __global__ void __launch_bounds__(32 * kWarps) packed_simt_kernel(const T* __res
     const float inv = lim[r] > 0 ? 1.0f / l[r] : 0.0f;
 #pragma unroll
     for (int c = 0; c < HD / 32; ++c)
-      out[tok * ld.out + h * HD + c * 32 + lane] = static_cast<T>(lim[r] > 0 ? acc[r][c] * inv : 0.0f);
+      out[tok * ld.out + h * HD + c * 32 + lane] = lim[r] > 0 ? acc[r][c] * inv : 0.0f;
     if (lse && lane == 0) lse[tok * n_heads + h] = lim[r] > 0 ? m[r] + logf(l[r]) : -INFINITY;
   }
 }
 
-template <typename T, int HD, int N>
+template <int HD, int N>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   PackedSeqs<N> s;
   const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, s);
@@ -214,28 +202,26 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   static std::atomic<bool> attr_set[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(packed_simt_kernel<T, HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(packed_f32_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  packed_simt_kernel<T, HD, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
-      static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), static_cast<T*>(a.out), a.lse,
+  packed_f32_kernel<HD, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
+      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
       Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, a.n_heads, a.n_heads / a.n_kv_heads, a.softmax_scale, a.causal);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_t(const PackedArgs& a, cudaStream_t st) {
-  if (a.n_seqs <= kFewSeqs)
-    return a.head_dim == 64 ? launch_n<T, 64, kFewSeqs>(a, st) : launch_n<T, 128, kFewSeqs>(a, st);
-  return a.head_dim == 64 ? launch_n<T, 64, DP_MAX_SEQS>(a, st) : launch_n<T, 128, DP_MAX_SEQS>(a, st);
+cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
+  if (a.n_seqs <= kFewSeqs) return a.head_dim == 64 ? launch_n<64, kFewSeqs>(a, st) : launch_n<128, kFewSeqs>(a, st);
+  return a.head_dim == 64 ? launch_n<64, DP_MAX_SEQS>(a, st) : launch_n<128, DP_MAX_SEQS>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s) {
   if (a.n_seqs < 1 || a.n_seqs > DP_MAX_SEQS || (a.head_dim != 64 && a.head_dim != 128)) return cudaErrorInvalidValue;
-  if (a.dt == DP_F32) return launch_t<float>(a, s);
+  if (a.dt == DP_F32) return launch_f32(a, s);
   // few rows: bound by reading the keys, which the kernel for few rows does at twice the rate
   const int group = a.n_heads / a.n_kv_heads;
   bool few = true;
