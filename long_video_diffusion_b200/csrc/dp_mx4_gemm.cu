@@ -105,13 +105,12 @@ __device__ __forceinline__ void store4(const Mx4Params& p, int64_t at, float4 v)
 
 template <int NT>  // tokens per tile
 struct Narrow {
-  static constexpr int RB = NT > 128 ? NT / 128 : 1;  // scale tiles of the tokens
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int A_BYTES = NT * 128;
   static constexpr int OFF_A = W_BYTES;
   static constexpr int OFF_SW = OFF_A + A_BYTES;
   static constexpr int OFF_SA = OFF_SW + 2 * kScaleTile;
-  static constexpr int STAGE = OFF_SA + 2 * kScaleTile * RB;
+  static constexpr int STAGE = OFF_SA + 2 * kScaleTile;
   static constexpr int STAGES = 4;
   static constexpr int PITCH = 128 + 4;  // floats between two tokens of the sums in shared memory
   static constexpr int SUMS = NT * PITCH * 4;
@@ -119,7 +118,7 @@ struct Narrow {
   static constexpr int N_BAR = 2 * STAGES + 1;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  static constexpr int SF_COLS = 8 + 8 * RB;  // columns of a step's scales: W's, then the tokens'
+  static constexpr int SF_COLS = 16;  // columns of a step's scales: W's, then the tokens'
   static constexpr int COL_SF = NT < 32 ? 32 : NT;
   static constexpr int COLS = COL_SF + STAGES * SF_COLS;  // a range of scales per stage
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
@@ -204,22 +203,22 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t sw = tmem + L::COL_SF + s * L::SF_COLS;
+      // a scale tile is of 128 rows, 32 to a column: the second 64 tokens' start two columns on
       const uint32_t sa = sw + 8;
+      const uint32_t sa_mine = sa + (NT == 64 ? (m_tile & 1) * 2 : 0);
       const uint32_t so = (s * L::STAGE) >> 4;
       const int chunks = min(4, (p.k - (first + i) * kStepK + 63) / 64);  // of 64: those behind k are zeros
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           cp_scales(sw + c * 4, sdesc_add(dsw, so + c * (kScaleTile >> 4)));
-#pragma unroll
-          for (int r = 0; r < L::RB; ++r)
-            cp_scales(sa + (c * L::RB + r) * 4, sdesc_add(dsa, so + (r * 2 + c) * (kScaleTile >> 4)));
+          cp_scales(sa + c * 4, sdesc_add(dsa, so + c * (kScaleTile >> 4)));
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (c < chunks)
             mma_mx4(tmem, sdesc_add(dw, so + c * 2), sdesc_add(da, so + c * 2), idesc_mx4(128, NT, (c & 1) * 2), sw + (c >> 1) * 4,
-                    sa + (c >> 1) * 4 * L::RB, (i > 0 || c > 0) ? 1u : 0u);
+                    sa_mine + (c >> 1) * 4, (i > 0 || c > 0) ? 1u : 0u);
         mma_commit(empty(s));
       }
       __syncwarp();
@@ -754,10 +753,17 @@ cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
 
 cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s) {
   if (g.m <= 0 || g.n <= 0 || g.n % 8 || g.k <= 0 || g.k % 32) return cudaErrorInvalidValue;
-  if (g.m > 256) return launch_wide(g, s);
+  // Few tokens: one tile of them.  More: tiles of 64, as long as their blocks fit on the SMs at once
+  // (two on each); then block pairs.  Measured with n x k = 4608 x 1536 and 4096 x 4096, us, tiles of
+  // 64 | pairs: m = 64 7.0 | 7.9, 7.0 | 10.8; m = 512 (288 and 256 blocks) 8.2 | 8.6, 11.4 | 11.7;
+  // m = 768 12.9 | 8.8, 18.5 | 11.8.  Tiles of 128 or 256 tokens were nowhere faster.
   if (g.m <= 16) return launch_narrow<16>(g, s);
-  if (g.m <= 64) return launch_narrow<64>(g, s);
-  return launch_narrow<128>(g, s);
+  if (g.m <= 32) return launch_narrow<32>(g, s);
+  int dev = 0, sms = 148;
+  const cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (g.m + 63) / 64 * ((static_cast<int64_t>(g.n) + 127) / 128);
+  return blocks <= 2 * sms ? launch_narrow<64>(g, s) : launch_wide(g, s);
 }
 
 }  // namespace dp
