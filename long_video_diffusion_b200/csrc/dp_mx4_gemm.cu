@@ -85,8 +85,7 @@ struct Mx4Params {
   void* y;
   int64_t m;
   int32_t n, k;
-  int32_t n_tiles;  // tiles of features
-  int32_t splits;   // blocks per cluster: parts of k
+  int32_t log_splits;  // log2 of the blocks per cluster: parts of k
   int32_t y_dt;
   uint32_t* status;
 };
@@ -135,11 +134,11 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % p.splits;
-  const int tile = blockIdx.x / p.splits;
-  const int n_tile = tile % p.n_tiles, m_tile = tile / p.n_tiles;
+  const int splits = 1 << p.log_splits;  // blocks of the cluster
+  const int rank = blockIdx.x & (splits - 1);
+  const int n_tile = blockIdx.x >> p.log_splits, m_tile = blockIdx.y;
   const int steps = (p.k + kStepK - 1) / kStepK;
-  const int per = (steps + p.splits - 1) / p.splits;
+  const int per = (steps + splits - 1) >> p.log_splits;
   const int first = rank * per;
   const int n_loc = max(0, min(per, steps - first));
 
@@ -149,7 +148,18 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
   const uint32_t acc_full = bar0 + 8u * (2 * L::STAGES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  if (threadIdx.x == 0) {
+  auto load_step = [&](int i) {
+    const int s = i % L::STAGES;
+    const uint32_t st = sb + s * L::STAGE;
+    const int kb = first + i;
+    mbar_arrive_expect_tx(full(s), L::STAGE);
+    tma_load_2d(st, &tm_w, kb * 128, n_tile * 128, full(s));
+    tma_load_3d(st + L::OFF_SW, &tm_sw, 0, kb * 2, n_tile, full(s));
+    tma_load_2d(st + L::OFF_A, &tm_a, kb * 128, m_tile * NT, full(s));
+    tma_load_3d(st + L::OFF_SA, &tm_sa, 0, kb * 2, m_tile * NT / 128, full(s));
+  };
+  int issued = 0;
+  if (warp == 0 && lane == 0) {
     for (int s = 0; s < L::STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -157,16 +167,12 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
     mbar_init(acc_full, 1);
     *abort = 0;
     fence_mbar_init();
+    // the first stages' loads, before the other warps are up
+    for (; issued < min(n_loc, L::STAGES); ++issued) load_step(issued);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
     tmem_relinquish();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_w);
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_sw);
-    tma_prefetch_desc(&tm_sa);
   }
   tc_fence_before();
   __syncthreads();
@@ -175,18 +181,9 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n_loc; ++i) {
-        const int s = i % L::STAGES;
-        if (i >= L::STAGES && !mbar_wait(empty(s), ((i / L::STAGES) - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
-        const uint32_t st = sb + s * L::STAGE;
-        const int kb = first + i;
-        mbar_arrive_expect_tx(full(s), L::STAGE);
-        tma_load_2d(st, &tm_w, kb * 128, n_tile * 128, full(s));
-        tma_load_3d(st + L::OFF_SW, &tm_sw, 0, kb * 2, n_tile, full(s));
-        tma_load_2d(st + L::OFF_A, &tm_a, kb * 128, m_tile * NT, full(s));
-        tma_load_3d(st + L::OFF_SA, &tm_sa, 0, kb * 2, m_tile * NT / 128, full(s));
-        issued = i + 1;
+      for (; issued < n_loc; ++issued) {
+        if (!mbar_wait(empty(issued % L::STAGES), (issued / L::STAGES - 1) & 1, abort, p.status, DEV_ERR_TIMEOUT_EMPTY)) break;
+        load_step(issued);
       }
       const int from = issued > L::STAGES ? issued - L::STAGES : 0;
       for (int i = from; i < issued; ++i) mbar_drain_wait(full(i % L::STAGES), (i / L::STAGES) & 1, p.status);
@@ -254,31 +251,31 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
     tc_fence_after();
     tmem_dealloc(tmem, L::TMEM_COLS);
   }
-  if (p.splits > 1) cluster_sync();
+  if (splits > 1) cluster_sync();
   // this block's share of the tile's tokens x 32 groups of four features
   const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), p.m - static_cast<int64_t>(m_tile) * NT));
-  const int share = (tokens * 32 + p.splits - 1) / p.splits;
+  const int share = (tokens * 32 + splits - 1) >> p.log_splits;
   const int end = min(tokens * 32, (rank + 1) * share);
   for (int i = rank * share + threadIdx.x; i < end; i += L::kThreads) {
     const int f = (i & 31) * 4, col = n_tile * 128 + f, t = i >> 5;
     if (col >= p.n) continue;
     float4 v = p.bias ? *reinterpret_cast<const float4*>(p.bias + col) : make_float4(0, 0, 0, 0);
     const uint32_t at = (t * L::PITCH + f) * 4;
-    if (p.splits == 1) {
+    if (splits == 1) {
       const float4 x = *reinterpret_cast<const float4*>(smem + at);
       v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
     } else {
       float4 x[kMaxSplits];
 #pragma unroll
       for (int s = 0; s < kMaxSplits; ++s)
-        if (s < p.splits) x[s] = ld_peer4(sb + at, s);
+        if (s < splits) x[s] = ld_peer4(sb + at, s);
 #pragma unroll
       for (int s = 0; s < kMaxSplits; ++s)
-        if (s < p.splits) v.x += x[s].x, v.y += x[s].y, v.z += x[s].z, v.w += x[s].w;
+        if (s < splits) v.x += x[s].x, v.y += x[s].y, v.z += x[s].z, v.w += x[s].w;
     }
     store4(p, (static_cast<int64_t>(m_tile) * NT + t) * p.n + col, v);
   }
-  if (p.splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
+  if (splits > 1) cluster_sync();  // no block leaves while another reads its shared memory
 }
 
 // ------------------------------------------------------------------ many rows of a
@@ -675,25 +672,26 @@ cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
   p.m = g.m;
   p.n = g.n;
   p.k = g.k;
-  p.n_tiles = (g.n + 127) / 128;
   p.y_dt = g.y_dt;
   p.status = g.status;
-  const int64_t tiles = (g.m + NT - 1) / NT * p.n_tiles;
+  const int64_t m_tiles = (g.m + NT - 1) / NT, n_tiles = (static_cast<int64_t>(g.n) + 127) / 128;
   const int steps = (g.k + kStepK - 1) / kStepK;
-  p.splits = 1;
-  while (p.splits < kMaxSplits && tiles * p.splits * 2 <= sms && steps >= p.splits * 2) p.splits *= 2;
-  if (tiles * p.splits > INT_MAX) return cudaErrorInvalidValue;
+  // as many parts of k as the SMs take at once, each of a step at least
+  int splits = 1;
+  p.log_splits = 0;
+  while (splits < kMaxSplits && m_tiles * n_tiles * splits * 2 <= sms && steps >= splits * 2) splits *= 2, ++p.log_splits;
+  if (m_tiles > 65535 || n_tiles * splits > INT_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::ALLOC;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.x = splits;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, mx4_narrow_kernel<NT>, tw, ta, tsw, tsa, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -734,8 +732,7 @@ cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
   w.p.m = g.m;
   w.p.n = g.n;
   w.p.k = g.k;
-  w.p.n_tiles = 0;
-  w.p.splits = 1;
+  w.p.log_splits = 0;
   w.p.y_dt = g.y_dt;
   w.p.status = g.status;
   const int64_t m_tiles = (g.m + 255) / 256, n_tiles = (g.n + 255) / 256;
