@@ -514,7 +514,7 @@ dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, cons
  * and lse = -infinity.
  * q, out: DEVICE [q_rows][n_heads][head_dim], k, v: DEVICE [k_rows][n_kv_heads][head_dim], all
  * of dt, rows ld_* elements apart (so that they may be column ranges of one buffer; multiples
- * of 16 bytes); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
+ * of 16 bytes, at most 2^28 elements); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
  * sequence are neither read nor written, key rows of no sequence affect nothing, whatever they
  * hold.  The rows of a sequence have to be finite: a value that the causal mask hides takes
  * part in a product with weight 0.

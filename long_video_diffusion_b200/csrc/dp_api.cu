@@ -1112,7 +1112,7 @@ dp_status dp_packed_attention(const void* q, int64_t ld_q, const void* k, int64_
   }
   const int64_t eb = elem_bytes(dt);
   const int64_t wq = static_cast<int64_t>(n_heads) * head_dim, wk = static_cast<int64_t>(n_kv_heads) * head_dim;
-  const int64_t most_ld = int64_t(1) << 31;
+  const int64_t most_ld = int64_t(1) << 28;
   if (ld_q < wq || ld_out < wq || ld_k < wk || ld_v < wk || ld_q > most_ld || ld_out > most_ld || ld_k > most_ld || ld_v > most_ld)
     return fail(DP_ERR_INVALID_ARG, "row pitches %lld %lld %lld %lld", static_cast<long long>(ld_q),
                 static_cast<long long>(ld_k), static_cast<long long>(ld_v), static_cast<long long>(ld_out));

@@ -189,6 +189,10 @@ struct PackedArgs {
 };
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s);
 
+// The current device (ordinal < 64) and its SMs; makes its context the calling thread's, which the
+// tensor-map encoder needs and a thread that has called nothing yet lacks (defined in dp_packed.cu).
+cudaError_t device_and_sms(int* dev, int* sms);
+
 // The driver's tensor-map encoder, NULL if it has none (defined in dp_attn_tc.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

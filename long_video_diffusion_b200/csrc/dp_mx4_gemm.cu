@@ -642,24 +642,17 @@ bool encode_out(EncodeFn fn, CUtensorMap* t, void* y, int64_t m, int32_t n, dp_d
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t device_sms(int* dev, int* sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return e;
-  if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-}
-
 template <int NT>
 cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
   using L = Narrow<NT>;
+  int dev = 0, sms = 148;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
   EncodeFn fn = tensor_map_encoder();
   CUtensorMap tw, ta, tsw, tsa;
   if (!fn || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) || !encode_codes(fn, &ta, g.a, g.m, g.k, NT) ||
       !encode_scales(fn, &tsw, g.w_scales, g.n, g.k, 128) || !encode_scales(fn, &tsa, g.a_scales, g.m, g.k, NT))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaError_t e = device_sms(&dev, &sms);
-  if (e != cudaSuccess) return e;
   static std::atomic<bool> attr_set[64];
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(mx4_narrow_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
@@ -698,14 +691,14 @@ cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
 
 cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
   using L = Wide;
+  int dev = 0, sms = 148;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
   EncodeFn fn = tensor_map_encoder();
   CUtensorMap ta, tw, tsa, tsw, ty;
   if (!fn || !encode_out(fn, &ty, g.y, g.m, g.n, g.y_dt) || !encode_codes(fn, &ta, g.a, g.m, g.k, 128) || !encode_codes(fn, &tw, g.w, g.n, g.k, 128) ||
       !encode_scales(fn, &tsa, g.a_scales, g.m, g.k, 128) || !encode_scales(fn, &tsw, g.w_scales, g.n, g.k, 256))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaError_t e = device_sms(&dev, &sms);
-  if (e != cudaSuccess) return e;
   static std::atomic<int> pairs_of[64];  // pairs that fit on the device at once
   int most = pairs_of[dev].load(std::memory_order_acquire);
   if (!most) {
@@ -757,7 +750,7 @@ cudaError_t launch_mx4_linear(const Mx4Args& g, cudaStream_t s) {
   if (g.m <= 16) return launch_narrow<16>(g, s);
   if (g.m <= 32) return launch_narrow<32>(g, s);
   int dev = 0, sms = 148;
-  const cudaError_t e = device_sms(&dev, &sms);
+  const cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (g.m + 63) / 64 * ((static_cast<int64_t>(g.n) + 127) / 128);
   return blocks <= 2 * sms ? launch_narrow<64>(g, s) : launch_wide(g, s);

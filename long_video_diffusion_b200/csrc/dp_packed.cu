@@ -55,9 +55,11 @@ bool encode_packed_kv(const PackedArgs& a, int box_rows, bool f16, CUtensorMap* 
 }
 
 cudaError_t device_and_sms(int* dev, int* sms) {
-  const cudaError_t e = cudaGetDevice(dev);
+  cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return e;
   if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  e = cudaSetDevice(*dev);
+  if (e != cudaSuccess) return e;
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
 }
 

@@ -124,8 +124,6 @@ Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, in
 // Tensor maps of k and v with boxes of `box_rows` keys by 64 columns.
 bool encode_packed_kv(const PackedArgs& a, int box_rows, bool f16, CUtensorMap* tk, CUtensorMap* tv);
 
-cudaError_t device_and_sms(int* dev, int* sms);  // the current device (ordinal < 64) and its SMs
-
 // One block per item or part of one.
 template <typename K, typename... A>
 cudaError_t launch_items(K kernel, const Cut& cut, int64_t items, int threads, int smem, cudaStream_t s, const A&... args) {

@@ -351,11 +351,11 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   PackedSeqs<N> seqs;
   const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, seqs);
   if (tiles != a.n_seqs || tiles * a.n_kv_heads > INT_MAX) return cudaErrorInvalidValue;
-  CUtensorMap tk, tv;
-  if (!encode_packed_kv(a, kKeys, F16, &tk, &tv)) return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
   cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
+  CUtensorMap tk, tv;
+  if (!encode_packed_kv(a, kKeys, F16, &tk, &tv)) return cudaErrorInvalidValue;
   auto kernel = packed_few_kernel<HD, F16, N>;
   static std::atomic<bool> attr_set[64];
   if (!attr_set[dev].load(std::memory_order_acquire)) {

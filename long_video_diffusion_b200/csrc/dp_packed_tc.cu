@@ -916,6 +916,9 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   PackedSeqs<N> seqs;
   const int64_t tiles = plan_packed(a, 1, NQ * p.tokens, seqs);
   if (tiles < 0 || tiles * p.n_kv > INT_MAX) return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv, to;
   int64_t q_rows = 0;
   for (int i = 0; i < a.n_seqs; ++i) {
@@ -925,9 +928,6 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   if (!encode_packed_kv(a, L::BN, F16, &tk, &tv) || !encode_tmap_16_heads(&tq, a.q, q_rows, a.n_heads, HD, a.ld_q, p.cut_heads, p.tokens, F16) ||
       !encode_tmap_16_heads(&to, a.out, q_rows, a.n_heads, HD, a.ld_out, p.cut_heads, p.tokens, F16))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaError_t e = device_and_sms(&dev, &sms);
-  if (e != cudaSuccess) return e;
   auto kernel = packed_attn_tc_kernel<HD, F16, N>;
   static std::atomic<bool> attr_set[64];
   if (!attr_set[dev].load(std::memory_order_acquire)) {

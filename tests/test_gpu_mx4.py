@@ -107,7 +107,8 @@ def _check_product(dp, m, n, k, bias, dtype, seed=0):
     (1, 8, 32, False), (1, 4096, 4096, True), (2, 136, 96, True), (16, 128, 256, False), (17, 1024, 1536, True),
     (33, 264, 544, False), (64, 512, 2048, True), (65, 72, 64, True), (100, 640, 224, False), (128, 256, 1024, True),
     (129, 264, 160, True), (255, 1000, 288, False), (256, 4608, 1536, True), (257, 120, 4128, True),
-    (300, 2048, 512, False), (513, 776, 1120, True), (1000, 520, 192, True)])
+    (300, 2048, 512, False), (513, 776, 1120, True), (1000, 520, 192, True), (32, 2056, 736, True), (448, 1160, 352, True),
+    (700, 6152, 96, False), (257, 20000, 64, True)])
 def test_linear_within_rounding(dp, m, n, k, bias, dtype):
     _check_product(dp, m, n, k, bias, dtype)
 
@@ -175,6 +176,20 @@ def test_captured_and_replayed_with_new_inputs(dp, m):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_first_call_of_a_thread(dp):
+    """A thread that has made no CUDA call yet."""
+    import threading
+    c, w = (_quantize(dp, _rows(n, 512, torch.bfloat16, n).cuda()) for n in (70, 264))
+    ys = [torch.zeros(70, 264, device="cuda") for _ in range(2)]
+    dp.mx4_linear(*c, *w, None, ys[0])
+    torch.cuda.synchronize()
+    t = threading.Thread(target=lambda: dp.mx4_linear(*c, *w, None, ys[1]))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert torch.equal(*ys)
 
 
 def test_no_rows_do_nothing(dp):

@@ -191,6 +191,43 @@ def test_many_sequences(dp, n):
         _check(out, lse, q, k, v, lens, k_lens, None, True)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_items_than_blocks_fit(dp, d, causal):
+    """Far more (tile, k/v head) items than the SMs hold blocks, so that blocks go on from one to
+    the next: sequences without keys, of one token and with every tail of a key tile among them."""
+    rng = np.random.default_rng(d)
+    lens = [int(x) for x in rng.integers(0, 90, 150)] + [0, 1, 400, 17]
+    k_lens = [int(x) for x in rng.integers(0, 200, 150)] + [5, 0, 700, 64]
+    q, k, v = _inputs(lens, k_lens, 12, 4, d, F16)
+    out, lse = _run(dp, q, k, v, lens, k_lens, None, causal)
+    _check(out, lse, q, k, v, lens, k_lens, None, causal)
+    again, _ = _run(dp, q, k, v, lens, k_lens, None, causal)
+    assert torch.equal(out[:sum(lens)], again[:sum(lens)])
+
+
+def test_calls_of_two_threads(dp):
+    """Two threads, a stream each, several calls under way: no call depends on another."""
+    import threading
+    lens, k_lens = [1, 40, 200], [3000, 900, 200]
+    q, k, v = (t.cuda() for t in _inputs(lens, k_lens, 8, 2, 128, BF16, spare=0))
+    ref, _ = _run(dp, q, k, v, lens, k_lens)
+    torch.cuda.synchronize()
+    outs = [[torch.zeros_like(ref) for _ in range(20)] for _ in range(2)]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for o in outs[i]:
+                dp.packed_attention(q, k, v, lens, k_lens, o)
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(o, ref) for side in outs for o in side)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_long_sequence_last_rows(dp, dtype):
     """A 9000-token prompt: its last and first rows against the oracle, the whole finite and repeatable."""

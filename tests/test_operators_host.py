@@ -79,6 +79,7 @@ def test_packed_attention_checks(m):
     assert call(qr=-1) == bad and call(kr=1 << 31) == bad
     assert call(ld=(255, 128, 128, 256)) == bad and call(ld=(256, 127, 128, 256)) == bad
     assert call(ld=(260, 128, 128, 256)) == bad                                # 520 bytes: no multiple of 16
+    assert call(ld=(256, 1 << 29, 128, 256)) == bad
     for name in ("q", "k", "v", "out"):
         assert call(**{name: 0}) == bad
         assert call(**{name: FAKE + 8 * M + 8}) == bad
