@@ -100,15 +100,17 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restr
   constexpr bool kWide = sizeof(T) == 4;
   const Unit u = unit_of_thread(tiles);
   const int sub = threadIdx.x & 15;
+  // (bound by the issue slots as much as by the memory: one address, one row count, few selects)
+  const int rows = u.col < k ? static_cast<int>(min(n_rows - u.row0, static_cast<int64_t>(128))) : 0;  // this thread's: j * 32 < rows
+  const int64_t at = u.row0 * k + u.col;
+  const int64_t step = 32ll * k;
   uint4 raw[4][kWide ? 2 : 1];
-  bool in[4];
+  const T* src = x + at;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    in[j] = u.row0 + 32 * j < n_rows && u.col < k;
-    const uint4* src = reinterpret_cast<const uint4*>(x + (u.row0 + 32 * j) * k + u.col);
+  for (int j = 0; j < 4; ++j, src += step)
 #pragma unroll
-    for (int h = 0; h < (kWide ? 2 : 1); ++h) raw[j][h] = in[j] ? __ldcs(src + h) : make_uint4(0, 0, 0, 0);
-  }
+    for (int h = 0; h < (kWide ? 2 : 1); ++h)
+      raw[j][h] = 32 * j < rows ? __ldcs(reinterpret_cast<const uint4*>(src) + h) : make_uint4(0, 0, 0, 0);
   // each row's largest magnitude in its block of 32 (four threads), as fp32 bits
   uint32_t top[4];
   if constexpr (kWide) {
@@ -147,18 +149,19 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restr
     }
   }
   uint32_t mine = 0;  // this block's four scale bytes, row j's at byte j
+  uint32_t* dst = codes + (at >> 3);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t ex = (top[j] >> 23) & 255u;
-    const uint32_t byte = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-    mine |= byte << (8 * j);
-    if (in[j]) {
-      const float inv = __uint_as_float((ex == 255u ? 127u : 254u - byte) << 23);
+  for (int j = 0; j < 4; ++j, dst += step >> 3) {
+    const uint32_t ex = top[j] >> 23;  // no sign: at most 255
+    const uint32_t least = max(ex, 2u);
+    mine |= (ex == 255u ? 255u : least - 2u) << (8 * j);
+    if (32 * j < rows) {
+      const float inv = __uint_as_float((256u - least) << 23);  // 2^-e; with an infinity or NaN whatever
       float f[8];
       unpack8<T>(raw[j], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= inv;
-      codes[((u.row0 + 32 * j) * k + u.col) >> 3] = pack_e2m1x8(f);
+      *dst = pack_e2m1x8(f);
     }
   }
   // 4 x 4 bytes turned between the four blocks' threads: block b's thread gets row b's word
@@ -176,21 +179,24 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t
                                                                   T* __restrict__ y, int64_t n_rows, int k, int tiles) {
   const Unit u = unit_of_thread(tiles);
   if (u.row0 >= n_rows || u.col >= k) return;
+  const int rows = static_cast<int>(min(n_rows - u.row0, static_cast<int64_t>(128)));
+  const int64_t at = u.row0 * k + u.col;
+  const int64_t step = 32ll * k;
   const uint4 s4 = __ldg(reinterpret_cast<const uint4*>(scales + (mx4_scale_at(u.row0, u.tile * 4, tiles) >> 2)));
   const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
   uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = u.row0 + 32 * j < n_rows ? __ldg(codes + (((u.row0 + 32 * j) * k + u.col) >> 3)) : 0u;
+  for (int j = 0; j < 4; ++j) c[j] = 32 * j < rows ? __ldg(codes + (at >> 3) + j * (step >> 3)) : 0u;
+  T* d = y + at;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (u.row0 + 32 * j >= n_rows) break;
+  for (int j = 0; j < 4; ++j, d += step) {
+    if (32 * j >= rows) break;
     const uint32_t s = (sw[j] >> (8 * ((threadIdx.x & 15) >> 2))) & 255u;
     const float scale = s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s ? s << 23 : 0x00400000u);
     float f[8];
     unpack_e2m1x8(c[j], f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= scale;
-    T* d = y + (u.row0 + 32 * j) * k + u.col;
     if constexpr (sizeof(T) == 4) {
       reinterpret_cast<float4*>(d)[0] = make_float4(f[0], f[1], f[2], f[3]);
       reinterpret_cast<float4*>(d)[1] = make_float4(f[4], f[5], f[6], f[7]);
