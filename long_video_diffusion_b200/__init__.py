@@ -551,10 +551,13 @@ _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 def _device_of(*tensors) -> int:
     """The CUDA device index of the tensors (None left out), which have to be on one."""
-    devs = {t.get_device() for t in tensors if t is not None}
-    if len(devs) != 1 or -1 in devs:
+    dev = tensors[0].get_device()
+    if dev < 0:
         raise ValueError("tensors must live on one CUDA device")
-    return devs.pop()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must live on one CUDA device")
+    return dev
 
 
 def _launch(fn, where: str, dev: int, stream, args) -> None:
@@ -588,58 +591,65 @@ def mx4_empty(rows: int, k: int, device=None):
             torch.empty(mx4_scale_bytes(rows, k), dtype=torch.uint8, device=dev))
 
 
-def _mx4(codes: torch.Tensor, scales: torch.Tensor, what: str):
-    """(rows, k) of a 4-bit matrix, its buffers checked."""
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2:
-        raise ValueError(f"{what}: codes must be uint8 [rows, k / 2] and scales uint8")
+_U8 = torch.uint8
+
+
+def _mx4(codes: torch.Tensor, scales: torch.Tensor):
+    """(rows, k / 2) of a 4-bit matrix, its buffers checked."""
+    if codes.dtype is not _U8 or scales.dtype is not _U8:
+        raise ValueError("codes and scales must be uint8")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("tensor must be contiguous")
     rows, half = codes.shape
     if scales.numel() < (rows + 127 >> 7) * (half + 63 >> 6) * 512:
-        raise ValueError(f"{what}: scales hold fewer than mx4_scale_bytes({rows}, {2 * half}) bytes")
+        raise ValueError(f"scales hold fewer than mx4_scale_bytes({rows}, {2 * half}) bytes")
+    return rows, half
+
+
+def _code(t: torch.Tensor) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _mx4_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """(rows, k) of rows x and their 4-bit form, checked."""
+    rows, half = _mx4(codes, scales)
+    if x.shape != (rows, 2 * half) or not x.is_contiguous():
+        raise ValueError(f"codes [{rows}, {half}] belong to a contiguous [{rows}, {2 * half}], not {tuple(x.shape)}")
     return rows, 2 * half
-
-
-def _mx4_rows(where: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
-    """(device, rows, k, dtype) of rows x and their 4-bit form, checked."""
-    rows, k = _mx4(codes, scales, where)
-    if x.shape != (rows, k) or not x.is_contiguous():
-        raise ValueError(f"{where}: codes [{rows}, {k // 2}] belong to a contiguous [{rows}, {k}], not {tuple(x.shape)}")
-    return _device_of(x, codes, scales), rows, k, _CODES.get(x.dtype)
 
 
 def mx4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """x [rows][k] (bf16, f16 or f32) to microscaled 4-bit codes and scales (dp_mx4_quantize);
     codes uint8 [rows][k / 2], scales uint8 of at least mx4_scale_bytes(rows, k)."""
-    dev, rows, k, dt = _mx4_rows("mx4_quantize", x, codes, scales)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    _launch(_lib.dp_mx4_quantize, "dp_mx4_quantize", dev, stream, (x.data_ptr(), rows, k, dt, codes.data_ptr(), scales.data_ptr()))
+    rows, k = _mx4_rows(x, codes, scales)
+    _launch(_lib.dp_mx4_quantize, "dp_mx4_quantize", _device_of(x, codes, scales), stream,
+            (x.data_ptr(), rows, k, _code(x), codes.data_ptr(), scales.data_ptr()))
 
 
 def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """The values that codes and scales stand for (dp_mx4_dequantize); y [rows][k] bf16, f16 or f32."""
-    dev, rows, k, dt = _mx4_rows("mx4_dequantize", y, codes, scales)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {y.dtype}")
-    _launch(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", dev, stream, (codes.data_ptr(), scales.data_ptr(), rows, k, y.data_ptr(), dt))
+    rows, k = _mx4_rows(y, codes, scales)
+    _launch(_lib.dp_mx4_dequantize, "dp_mx4_dequantize", _device_of(y, codes, scales), stream,
+            (codes.data_ptr(), scales.data_ptr(), rows, k, y.data_ptr(), _code(y)))
 
 
 def mx4_linear(a, a_scales, w, w_scales, bias, y, stream=None) -> None:
     """y = a W^T + bias on 4-bit operands (dp_mx4_linear): a [m][k] and w [n][k] as codes and
     scales, bias float [n] or None, y [m][n] bf16, f16 or f32."""
-    m, k = _mx4(a, a_scales, "a")
-    n, kw = _mx4(w, w_scales, "w")
-    if kw != k or y.shape != (m, n) or not y.is_contiguous():
-        raise ValueError(f"a [{m}, {k}], w [{n}, {kw}] and a contiguous y {tuple(y.shape)} do not match")
-    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (n,) or not bias.is_contiguous()):
-        raise ValueError("bias must be float32 [n]")
-    dt = _CODES.get(y.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {y.dtype}")
+    m, half = _mx4(a, a_scales)
+    n, half_w = _mx4(w, w_scales)
+    if half_w != half or y.shape != (m, n) or not y.is_contiguous():
+        raise ValueError(f"a [{m}, {2 * half}], w [{n}, {2 * half_w}] and a contiguous y {tuple(y.shape)} do not match")
+    b = None
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.shape != (n,) or not bias.is_contiguous():
+            raise ValueError("bias must be float32 [n]")
+        b = bias.data_ptr()
     _launch(_lib.dp_mx4_linear, "dp_mx4_linear", _device_of(y, a, a_scales, w, w_scales, bias), stream,
-            (a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
-             m, n, k, y.data_ptr(), dt))
+            (a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), b, m, n, 2 * half, y.data_ptr(), _code(y)))
 
 
 # ------------------------------------------------------------------------- E: packed attention
@@ -667,10 +677,11 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
     n = len(q_lens)
     if len(k_lens) != n or (k_starts is not None and len(k_starts) != n):
         raise ValueError("q_lens, k_lens and k_starts differ in length")
-    if q.dim() != 3 or k.dim() != 3:
+    shape, k_shape = q.shape, k.shape
+    if len(shape) != 3 or len(k_shape) != 3:
         raise ValueError("q, k, v and out must be [rows, heads, head_dim]")
-    (rows, heads, d), (k_rows, kv_heads, dk) = q.shape, k.shape
-    if out.shape != q.shape or v.shape != k.shape or dk != d:
+    (rows, heads, d), (k_rows, kv_heads, dk) = shape, k_shape
+    if out.shape != shape or v.shape != k_shape or dk != d:
         raise ValueError("shapes of q and out, or of k and v, or their head_dim differ")
     lq, lk, lv, lo = _pitch(q, heads, d), _pitch(k, kv_heads, d), _pitch(v, kv_heads, d), _pitch(out, heads, d)
     dt = q.dtype
@@ -678,14 +689,11 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
         raise TypeError("q, k, v and out differ in dtype")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [q_rows, heads]")
-    code = _CODES.get(dt)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dt}")
     arr = _I64 * n
     _launch(_lib.dp_packed_attention, "dp_packed_attention", _device_of(q, k, v, out, lse), stream,
             (q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv, out.data_ptr(), lo, None if lse is None else lse.data_ptr(),
              rows, k_rows, arr(*q_lens), arr(*k_lens), None if k_starts is None else arr(*k_starts), n, heads, kv_heads, d,
-             softmax_scale, CAUSAL if causal else 0, code))
+             softmax_scale, CAUSAL if causal else 0, _code(q)))
 
 
 def profile_begin(max_steps: int) -> None:
