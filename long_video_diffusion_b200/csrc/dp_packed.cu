@@ -68,26 +68,39 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRowsPerWarp = 8;
 constexpr int kRows = kWarps * kRowsPerWarp;  // query rows per block
-constexpr int kKeys = 32;                     // keys per tile: one per lane
+constexpr int kKeys = 64;                     // keys per tile: two per lane
+
+template <int HD>
+struct F32Lay {
+  static constexpr int KP = HD + 4;       // pitch of a key row: 16-byte reads of 32 rows without conflicts
+  static constexpr int PP = kKeys + 4;    // pitch of a row of weights
+  static constexpr int OFF_V = kKeys * KP;
+  static constexpr int OFF_Q = OFF_V + kKeys * HD;
+  static constexpr int OFF_P = OFF_Q + kRows * HD;
+  static constexpr int FLOATS = OFF_P + kRows * PP;
+};
 
 struct Strides {
   int64_t q, k, v, out;
 };
 
-// A warp's eight rows against one tile of 32 keys: lane j holds key j's scores, then each lane
-// its columns of the output.
+// A warp's eight rows against a tile of 64 keys: a lane holds two keys' scores of each row, then,
+// with the weights in shared memory, HD / 32 columns of each row's output.  Either way a 16-byte
+// read from shared memory feeds at least four multiply-adds per lane, about what the two can take.
 template <int HD, int N>
 __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                                  const float* __restrict__ v, float* __restrict__ out,
                                                                  float* __restrict__ lse, Strides ld,
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
                                                                  int group, float scale, int causal) {
-  extern __shared__ float smem[];
-  constexpr int KP = HD + 4;  // pitch of a key row: 16-byte reads of 32 rows without conflicts
+  using L = F32Lay<HD>;
+  extern __shared__ __align__(16) float smem[];
+  constexpr int C = HD / 32;  // output columns per lane
   float* sk = smem;           // [kKeys][KP]
-  float* sv = sk + kKeys * KP;  // [kKeys][HD]
-  float* sq = sv + kKeys * HD;  // [kRows][HD], scaled
+  float* sv = smem + L::OFF_V;
+  float* sq = smem + L::OFF_Q;  // [kRows][HD], scaled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* sp = smem + L::OFF_P + warp * kRowsPerWarp * L::PP;
   const int tile = blockIdx.x, kv = blockIdx.y;
   const int s = seq_of_tile(seqs, tile);
   const int q_len = seqs.q_len[s], k_len = seqs.k_len[s];
@@ -103,11 +116,10 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
       const int tok = (row0 + r) / group, h = kv * group + (row0 + r) % group;
       x = *reinterpret_cast<const float4*>(q + (seqs.first_q[s] + static_cast<int64_t>(tok)) * ld.q + h * HD + c);
     }
-    float* d = sq + r * HD + c;
-    d[0] = x.x * scale, d[1] = x.y * scale, d[2] = x.z * scale, d[3] = x.w * scale;
+    *reinterpret_cast<float4*>(sq + r * HD + c) = make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
   }
   int lim[kRowsPerWarp];
-  float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][HD / 32];
+  float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][C];  // l: this lane's keys
 #pragma unroll
   for (int r = 0; r < kRowsPerWarp; ++r) {
     const int row = row0 + warp * kRowsPerWarp + r;
@@ -115,80 +127,93 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     m[r] = -INFINITY;
     l[r] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < HD / 32; ++c) acc[r][c] = 0.0f;
+    for (int c = 0; c < C; ++c) acc[r][c] = 0.0f;
   }
   for (int j0 = 0; j0 < seen; j0 += kKeys) {
     __syncthreads();
     for (int i = threadIdx.x; i < kKeys * (HD / 4); i += 32 * kWarps) {
       const int j = i / (HD / 4), c = (i % (HD / 4)) * 4;
       float4 x = make_float4(0, 0, 0, 0), y = x;
-      if (j0 + j < k_len) {
+      if (j0 + j < k_len) {  // rows behind the sequence count as zeros, whatever they hold
         const int64_t row = seqs.first_k[s] + static_cast<int64_t>(j0 + j);
         x = *reinterpret_cast<const float4*>(k + row * ld.k + kv * HD + c);
         y = *reinterpret_cast<const float4*>(v + row * ld.v + kv * HD + c);
       }
-      *reinterpret_cast<float4*>(sk + j * KP + c) = x;
+      *reinterpret_cast<float4*>(sk + j * L::KP + c) = x;
       *reinterpret_cast<float4*>(sv + j * HD + c) = y;
     }
     __syncthreads();
     if (warp * kRowsPerWarp >= n_rows) continue;
-    float dot[kRowsPerWarp] = {};
-    const float* kr = sk + lane * KP;
+    float dot[kRowsPerWarp][2] = {};
+    const float* k0 = sk + lane * L::KP;
     const float* qr = sq + warp * kRowsPerWarp * HD;
-#pragma unroll 4
+#pragma unroll 2
     for (int c = 0; c < HD; c += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(kr + c);
+      const float4 x = *reinterpret_cast<const float4*>(k0 + c);
+      const float4 z = *reinterpret_cast<const float4*>(k0 + 32 * L::KP + c);
 #pragma unroll
       for (int r = 0; r < kRowsPerWarp; ++r) {
         const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
-        dot[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r]))));
+        dot[r][0] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r][0]))));
+        dot[r][1] = fmaf(z.x, y.x, fmaf(z.y, y.y, fmaf(z.z, y.z, fmaf(z.w, y.w, dot[r][1]))));
       }
     }
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
-      const float x = j0 + lane < lim[r] ? dot[r] : -INFINITY;
-      float t = x;
+      const float x0 = j0 + lane < lim[r] ? dot[r][0] : -INFINITY;
+      const float x1 = j0 + 32 + lane < lim[r] ? dot[r][1] : -INFINITY;
+      float t = fmaxf(x0, x1);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
       const float mn = fmaxf(m[r], t);
-      const float ref = mn == -INFINITY ? 0.0f : mn;
+      const float ref = mn == -INFINITY ? 0.0f : mn;  // a row that has seen no key: weights 0
       const float f = expf(m[r] - ref);
-      const float p = expf(x - ref);
+      const float p0 = expf(x0 - ref), p1 = expf(x1 - ref);
       m[r] = mn;
-      float sum = p;
+      l[r] = l[r] * f + (p0 + p1);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l[r] = l[r] * f + sum;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) acc[r][c] *= f;
-      dot[r] = p;
+      for (int c = 0; c < C; ++c) acc[r][c] *= f;
+      sp[r * L::PP + lane] = p0;
+      sp[r * L::PP + 32 + lane] = p1;
     }
+    __syncwarp();
     const int n_keys = min(kKeys, seen - j0);
-    for (int j = 0; j < n_keys; ++j) {
-      float y[HD / 32];
+#pragma unroll 1
+    for (int j = 0; j < n_keys; j += 4) {  // (rows behind the sequence are zeros, weights behind `seen` too)
+      float y[4][C];
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) y[c] = sv[j * HD + c * 32 + lane];
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(sv + (j + e) * HD + lane * C + c);
+          y[e][c] = t.x;
+          y[e][c + 1] = t.y;
+        }
 #pragma unroll
       for (int r = 0; r < kRowsPerWarp; ++r) {
-        const float p = __shfl_sync(0xffffffffu, dot[r], j);
-        if (j0 + j < lim[r]) {  // uniform in the warp: what the mask hides is not multiplied
+        const float4 p = *reinterpret_cast<const float4*>(sp + r * L::PP + j);
 #pragma unroll
-          for (int c = 0; c < HD / 32; ++c) acc[r][c] = fmaf(p, y[c], acc[r][c]);
-        }
+        for (int c = 0; c < C; ++c)
+          acc[r][c] = fmaf(p.x, y[0][c], fmaf(p.y, y[1][c], fmaf(p.z, y[2][c], fmaf(p.w, y[3][c], acc[r][c]))));
       }
     }
+    __syncwarp();
   }
 #pragma unroll
   for (int r = 0; r < kRowsPerWarp; ++r) {
     const int row = row0 + warp * kRowsPerWarp + r;
     if (row >= rows) break;
+    float sum = l[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int64_t tok = seqs.first_q[s] + static_cast<int64_t>(row / group);
     const int h = kv * group + row % group;
-    const float inv = lim[r] > 0 ? 1.0f / l[r] : 0.0f;
+    const float inv = lim[r] > 0 ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int c = 0; c < HD / 32; ++c)
-      out[tok * ld.out + h * HD + c * 32 + lane] = lim[r] > 0 ? acc[r][c] * inv : 0.0f;
-    if (lse && lane == 0) lse[tok * n_heads + h] = lim[r] > 0 ? m[r] + logf(l[r]) : -INFINITY;
+    for (int c = 0; c < C; c += 2)
+      *reinterpret_cast<float2*>(out + tok * ld.out + h * HD + lane * C + c) =
+          lim[r] > 0 ? make_float2(acc[r][c] * inv, acc[r][c + 1] * inv) : make_float2(0.0f, 0.0f);
+    if (lse && lane == 0) lse[tok * n_heads + h] = lim[r] > 0 ? m[r] + logf(sum) : -INFINITY;
   }
 }
 
@@ -197,7 +222,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   PackedSeqs<N> s;
   const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, s);
   if (tiles < 0 || a.n_kv_heads > 65535) return cudaErrorInvalidValue;
-  constexpr int bytes = (kKeys * (HD + 4) + kKeys * HD + kRows * HD) * 4;
+  constexpr int bytes = F32Lay<HD>::FLOATS * 4;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
