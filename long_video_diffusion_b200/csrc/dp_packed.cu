@@ -66,12 +66,12 @@ cudaError_t device_and_sms(int* dev, int* sms) {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRowsPerWarp = 8;
-constexpr int kRows = kWarps * kRowsPerWarp;  // query rows per block
-constexpr int kKeys = 64;                     // keys per tile: two per lane
+constexpr int kKeys = 64;  // keys per tile: two per lane
 
-template <int HD>
+// RPW: query rows per warp.
+template <int HD, int RPW>
 struct F32Lay {
+  static constexpr int kRows = kWarps * RPW;  // per block
   static constexpr int KP = HD + 4;       // pitch of a key row: 16-byte reads of 32 rows without conflicts
   static constexpr int PP = kKeys + 4;    // pitch of a row of weights
   static constexpr int OFF_V = kKeys * KP;
@@ -84,23 +84,24 @@ struct Strides {
   int64_t q, k, v, out;
 };
 
-// A warp's eight rows against a tile of 64 keys: a lane holds two keys' scores of each row, then,
+// A warp's RPW rows against a tile of 64 keys: a lane holds two keys' scores of each row, then,
 // with the weights in shared memory, HD / 32 columns of each row's output.  Either way a 16-byte
-// read from shared memory feeds at least four multiply-adds per lane, about what the two can take.
-template <int HD, int N>
+// read from shared memory feeds two to four multiply-adds per lane.
+template <int HD, int RPW, int N>
 __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                                  const float* __restrict__ v, float* __restrict__ out,
                                                                  float* __restrict__ lse, Strides ld,
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
                                                                  int group, float scale, int causal) {
-  using L = F32Lay<HD>;
+  using L = F32Lay<HD, RPW>;
+  constexpr int kRows = L::kRows;
   extern __shared__ __align__(16) float smem[];
   constexpr int C = HD / 32;  // output columns per lane
   float* sk = smem;           // [kKeys][KP]
   float* sv = smem + L::OFF_V;
   float* sq = smem + L::OFF_Q;  // [kRows][HD], scaled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* sp = smem + L::OFF_P + warp * kRowsPerWarp * L::PP;
+  float* sp = smem + L::OFF_P + warp * RPW * L::PP;
   const int tile = blockIdx.x, kv = blockIdx.y;
   const int s = seq_of_tile(seqs, tile);
   const int q_len = seqs.q_len[s], k_len = seqs.k_len[s];
@@ -118,11 +119,11 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     }
     *reinterpret_cast<float4*>(sq + r * HD + c) = make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
   }
-  int lim[kRowsPerWarp];
-  float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][C];  // l: this lane's keys
+  int lim[RPW];
+  float m[RPW], l[RPW], acc[RPW][C];  // l: this lane's keys
 #pragma unroll
-  for (int r = 0; r < kRowsPerWarp; ++r) {
-    const int row = row0 + warp * kRowsPerWarp + r;
+  for (int r = 0; r < RPW; ++r) {
+    const int row = row0 + warp * RPW + r;
     lim[r] = row < rows ? min(k_len, keys_seen(row / group, q_len, k_len, causal)) : 0;
     m[r] = -INFINITY;
     l[r] = 0.0f;
@@ -143,23 +144,23 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
       *reinterpret_cast<float4*>(sv + j * HD + c) = y;
     }
     __syncthreads();
-    if (warp * kRowsPerWarp >= n_rows) continue;
-    float dot[kRowsPerWarp][2] = {};
+    if (warp * RPW >= n_rows) continue;
+    float dot[RPW][2] = {};
     const float* k0 = sk + lane * L::KP;
-    const float* qr = sq + warp * kRowsPerWarp * HD;
+    const float* qr = sq + warp * RPW * HD;
 #pragma unroll 2
     for (int c = 0; c < HD; c += 4) {
       const float4 x = *reinterpret_cast<const float4*>(k0 + c);
       const float4 z = *reinterpret_cast<const float4*>(k0 + 32 * L::KP + c);
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) {
+      for (int r = 0; r < RPW; ++r) {
         const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
         dot[r][0] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r][0]))));
         dot[r][1] = fmaf(z.x, y.x, fmaf(z.y, y.y, fmaf(z.z, y.z, fmaf(z.w, y.w, dot[r][1]))));
       }
     }
 #pragma unroll
-    for (int r = 0; r < kRowsPerWarp; ++r) {
+    for (int r = 0; r < RPW; ++r) {
       const float x0 = j0 + lane < lim[r] ? dot[r][0] : -INFINITY;
       const float x1 = j0 + 32 + lane < lim[r] ? dot[r][1] : -INFINITY;
       float t = fmaxf(x0, x1);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
           y[e][c + 1] = t.y;
         }
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) {
+      for (int r = 0; r < RPW; ++r) {
         const float4 p = *reinterpret_cast<const float4*>(sp + r * L::PP + j);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     __syncwarp();
   }
 #pragma unroll
-  for (int r = 0; r < kRowsPerWarp; ++r) {
-    const int row = row0 + warp * kRowsPerWarp + r;
+  for (int r = 0; r < RPW; ++r) {
+    const int row = row0 + warp * RPW + r;
     if (row >= rows) break;
     float sum = l[r];
 #pragma unroll
@@ -217,26 +218,41 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
   }
 }
 
-template <int HD, int N>
-cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
+template <int HD, int RPW, int N>
+cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
   PackedSeqs<N> s;
-  const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, kRows, s);
+  const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, F32Lay<HD, RPW>::kRows, s);
   if (tiles < 0 || a.n_kv_heads > 65535) return cudaErrorInvalidValue;
-  constexpr int bytes = F32Lay<HD>::FLOATS * 4;
+  constexpr int bytes = F32Lay<HD, RPW>::FLOATS * 4;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<bool> attr_set[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(packed_f32_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(packed_f32_kernel<HD, RPW, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  packed_f32_kernel<HD, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
+  packed_f32_kernel<HD, RPW, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
       static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
       Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, a.n_heads, a.n_heads / a.n_kv_heads, a.softmax_scale, a.causal);
   return cudaGetLastError();
+}
+
+// Four rows per warp, 32 per block; two while those blocks do not even fill the SMs once (single
+// tokens, short prompts).  Measured, us, two | four rows: one head over 512 tokens (16 blocks of 32
+// rows) 46 | 60, 4 of 3000 keys' single tokens (32) 285 | 357, eight k/v heads over 540 tokens (680)
+// 98 | 85, 2048 tokens x 16 heads (1024) 977 | 773.  Eight: 92, 500, 85, 817.
+template <int HD, int N>
+cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 148;
+  const cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  int64_t blocks = 0;
+  for (int i = 0; i < a.n_seqs; ++i)
+    blocks += (static_cast<int64_t>(a.q_len[i]) * (a.n_heads / a.n_kv_heads) + 31) / 32 * a.n_kv_heads;
+  return blocks >= sms ? launch_rows<HD, 4, N>(a, st) : launch_rows<HD, 2, N>(a, st);
 }
 
 cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
