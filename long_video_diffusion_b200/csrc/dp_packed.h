@@ -90,10 +90,12 @@ __device__ __forceinline__ ItemPart item_part(int log_cluster, int n_cut) {
 }
 
 // The cluster size, and with it which sequences' keys are cut, that promises the earliest end:
-// an even share of all key tiles, with `overhead` tiles for each block's start and end, over
-// `slots` blocks at a time, or the longest part, whichever is later.  per_tile: items per row tile.
+// an even share of all key tiles, with `whole` tiles for the start and end of a block with an item
+// of its own and `part` for those of a block with a part of one, over `slots` blocks at a time; or
+// the longest block, whichever is later.  per_tile: items per row tile.  (16 cases with every fixed
+// size: the chosen one within 6 % of the fastest, except where they differ by less than 2 us.)
 template <int N>
-Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, int slots, int overhead) {
+Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, int slots, int whole, int part) {
   auto key_tiles = [&](int i) { return (static_cast<int64_t>(s.k_len[i]) + bn - 1) / bn; };
   int64_t total = 0;
   for (int i = 0; i < s.n; ++i) {
@@ -107,12 +109,15 @@ Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, in
   Cut best = {1, 0};
   int64_t best_end = -1;
   for (int c = 1; c <= kMaxCluster && (c == 1 || most >= 2 * c); c *= 2) {
-    const int64_t part = (most + c - 1) / c;
+    const int64_t longest = (most + c - 1) / c;
     Cut now = {c, 0};
     if (c > 1)
-      for (int i = 0; i < s.n && key_tiles(i) > part; ++i) now.items = static_cast<int64_t>(s.tile0[i + 1]) * per_tile;
-    const int64_t share = (total + overhead * (items + now.items * (c - 1))) / slots;
-    const int64_t end = share > part + overhead ? share : part + overhead;
+      for (int i = 0; i < s.n && key_tiles(i) > longest; ++i) now.items = static_cast<int64_t>(s.tile0[i + 1]) * per_tile;
+    const int64_t blocks = items + now.items * (c - 1);
+    int64_t share = (total + whole * (items - now.items) + part * now.items * c) / slots;
+    if (blocks > slots) share = share * (8 + c) / 9;  // a cluster waits for all its blocks' places
+    const int64_t last = longest + (c > 1 ? part : whole);
+    const int64_t end = share > last ? share : last;
     if (best_end < 0 || end < best_end) {
       best = now;
       best_end = end;

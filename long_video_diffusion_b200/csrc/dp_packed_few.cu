@@ -364,7 +364,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
     attr_set[dev].store(true, std::memory_order_release);
   }
   const int64_t items = tiles * a.n_kv_heads;
-  const Cut cut = choose_cut(a.causal, seqs, a.n_kv_heads, kKeys, 2 * sms, kFewOverhead);
+  const Cut cut = choose_cut(a.causal, seqs, a.n_kv_heads, kKeys, 2 * sms, kFewOverhead, kFewOverhead);
   FewParams p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.out = static_cast<uint16_t*>(a.out);

@@ -77,7 +77,8 @@ struct Lay {
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int Q_BYTES = BM * HD * 2;
   static constexpr int KV_BYTES = BN * HD * 2;
-  static constexpr int kOverhead = 5;          // key tiles that a block's start and end cost
+  // key tiles that a block's start and end cost, and those of a block that joins parts
+  static constexpr int kWhole = HD == 64 ? 4 : 5, kPart = kWhole + 4;
   static constexpr bool S_PER_TILE = HD > BN;  // the issuers' split (see above)
   static constexpr int kPvIssuers = S_PER_TILE ? 1 : NQ;
   // Whether a block goes on with further items.  At head_dim 64 a row's 128 scores leave the softmax
@@ -944,7 +945,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.ld_out = a.ld_out;
   p.n_heads = a.n_heads;
   p.group = group;
-  const Cut cut = choose_cut(a.causal, seqs, p.n_kv, L::BN, sms, L::kOverhead);
+  const Cut cut = choose_cut(a.causal, seqs, p.n_kv, L::BN, sms, L::kWhole, L::kPart);
   p.by_kv = fast_div(p.n_kv);
   p.by_cut_heads = fast_div(p.cut_heads);
   p.log_cluster = cut.log_cluster();
