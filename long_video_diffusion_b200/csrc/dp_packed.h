@@ -70,12 +70,13 @@ constexpr int kFewSeqs = 32;  // launches of up to this many sequences carry a s
 // An item is a tile of rows under one k/v head, k/v heads fastest.  The keys of the first
 // n_cut items are cut into as many parts as a cluster has blocks; the clusters behind theirs
 // take one whole item per block.
-constexpr int kMaxCluster = 8;  // portable cluster size
+constexpr int kMaxCluster = 8;   // portable cluster size
+constexpr int kFewCluster = 16;  // the largest there is, for the kernel for few rows
 
 struct Cut {
   int cluster;  // a power of two
   int64_t items;
-  int log_cluster() const { return cluster == 8 ? 3 : cluster == 4 ? 2 : cluster == 2 ? 1 : 0; }
+  int log_cluster() const { return cluster == 16 ? 4 : cluster == 8 ? 3 : cluster == 4 ? 2 : cluster == 2 ? 1 : 0; }
 };
 
 struct ItemPart {
@@ -93,9 +94,9 @@ __device__ __forceinline__ ItemPart item_part(int log_cluster, int n_cut) {
 // an even share of all key tiles, with `whole` tiles for the start and end of a block with an item
 // of its own and `part` for those of a block with a part of one, over `slots` blocks at a time; or
 // the longest block, whichever is later.  per_tile: items per row tile.  (16 cases with every fixed
-// size: the chosen one within 6 % of the fastest, except where they differ by less than 2 us.)
+// size up to 8: the chosen one within 6 % of the fastest.)
 template <int N>
-Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, int slots, int whole, int part) {
+Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, int slots, int whole, int part, int most_parts) {
   auto key_tiles = [&](int i) { return (static_cast<int64_t>(s.k_len[i]) + bn - 1) / bn; };
   int64_t total = 0;
   for (int i = 0; i < s.n; ++i) {
@@ -108,7 +109,7 @@ Cut choose_cut(bool causal, const PackedSeqs<N>& s, int64_t per_tile, int bn, in
   const int64_t most = key_tiles(0);
   Cut best = {1, 0};
   int64_t best_end = -1;
-  for (int c = 1; c <= kMaxCluster && (c == 1 || most >= 2 * c); c *= 2) {
+  for (int c = 1; c <= most_parts && (c == 1 || most >= 2 * c); c *= 2) {
     const int64_t longest = (most + c - 1) / c;
     Cut now = {c, 0};
     if (c > 1)

@@ -39,7 +39,7 @@ struct Few {
   static constexpr int STAGES = HD == 128 ? 3 : 5;
   static constexpr int OFF_JOIN = STAGES * STAGE;   // what the cluster's blocks send: [part][row][HD / parts], then (m, l)
   static constexpr int OFF_ML = OFF_JOIN + kRows * HD * 4;
-  static constexpr int OFF_WML = OFF_ML + kMaxCluster * kRows * 8;  // the warps' (m, l)
+  static constexpr int OFF_WML = OFF_ML + kFewCluster * kRows * 8;  // the warps' (m, l)
   static constexpr int OFF_BAR = OFF_WML + kWarps * kRows * 8;
   static constexpr int OFF_MISC = OFF_BAR + 2 * STAGES * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
@@ -361,10 +361,12 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
   const int64_t items = tiles * a.n_kv_heads;
-  const Cut cut = choose_cut(a.causal, seqs, a.n_kv_heads, kKeys, 2 * sms, kFewOverhead, kFewOverhead);
+  const Cut cut = choose_cut(a.causal, seqs, a.n_kv_heads, kKeys, 2 * sms, kFewOverhead, kFewOverhead, kFewCluster);
   FewParams p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.out = static_cast<uint16_t*>(a.out);

@@ -945,7 +945,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t s) {
   p.ld_out = a.ld_out;
   p.n_heads = a.n_heads;
   p.group = group;
-  const Cut cut = choose_cut(a.causal, seqs, p.n_kv, L::BN, sms, L::kWhole, L::kPart);
+  const Cut cut = choose_cut(a.causal, seqs, p.n_kv, L::BN, sms, L::kWhole, L::kPart, kMaxCluster);
   p.by_kv = fast_div(p.n_kv);
   p.by_cut_heads = fast_div(p.cut_heads);
   p.log_cluster = cut.log_cluster();
