@@ -48,6 +48,13 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
+// Programmatic dependent launch.  A kernel launched so may start before the kernels before it in
+// the stream have ended; it waits here before it touches any memory of the caller's.
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The next kernel's blocks may come as soon as all of this one's have got here (they wait as above).
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -140,6 +140,40 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s);
 cudaError_t launch_ln_modulate(const void* x, void* h, int64_t n_rows, int hidden, float eps, const BlockTable& bt,
                                cudaStream_t s);
 
+// Launches a kernel that begins with wait_for_earlier_kernels(): outside stream capture its blocks
+// may be placed while the stream's kernel before it ends (in a captured graph the edges would be
+// programmatic ones, which not every graph takes).  cluster: blocks per cluster along x, 1 for none.
+template <typename K, typename... A>
+cudaError_t launch_early(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    cudaGetLastError();
+    capture = cudaStreamCaptureStatusActive;
+  }
+  if (capture == cudaStreamCaptureStatusNone) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Microscaled 4-bit rows (dp_mx4.cu).  Scale byte of block b of row r; tiles = ceil(k / 128).
 __host__ __device__ __forceinline__ int64_t mx4_scale_at(int64_t r, int32_t b, int32_t tiles) {
   return ((r >> 7) * tiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);

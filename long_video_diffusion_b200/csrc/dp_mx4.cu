@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restr
                                                                 uint32_t* __restrict__ scales, int64_t n_rows, int k,
                                                                 int tiles) {
   constexpr bool kWide = sizeof(T) == 4;
+  let_next_kernel_start();
+  wait_for_earlier_kernels();
   const Unit u = unit_of_thread(tiles);
   const int sub = threadIdx.x & 15;
   // (bound by the issue slots as much as by the memory: one address, one row count, few selects)
@@ -177,6 +179,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                                   const uint32_t* __restrict__ scales,
                                                                   T* __restrict__ y, int64_t n_rows, int k, int tiles) {
+  let_next_kernel_start();
+  wait_for_earlier_kernels();
   const Unit u = unit_of_thread(tiles);
   if (u.row0 >= n_rows || u.col >= k) return;
   const int rows = static_cast<int>(min(n_rows - u.row0, static_cast<int64_t>(128)));
@@ -217,19 +221,17 @@ template <typename T>
 cudaError_t quantize(const void* x, int64_t n_rows, int32_t k, void* codes, void* scales, cudaStream_t s) {
   const int64_t grid = mx4_grid(n_rows, k);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  mx4_quantize_kernel<T><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
-      static_cast<const T*>(x), static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), n_rows, k, (k + 127) / 128);
-  return cudaGetLastError();
+  return launch_early(mx4_quantize_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, s, static_cast<const T*>(x),
+                      static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), n_rows, static_cast<int>(k), (k + 127) / 128);
 }
 
 template <typename T>
 cudaError_t dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y, cudaStream_t s) {
   const int64_t grid = mx4_grid(n_rows, k);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  mx4_dequantize_kernel<T><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
-      static_cast<const uint32_t*>(codes), static_cast<const uint32_t*>(scales), static_cast<T*>(y), n_rows, k,
-      (k + 127) / 128);
-  return cudaGetLastError();
+  return launch_early(mx4_dequantize_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, s,
+                      static_cast<const uint32_t*>(codes), static_cast<const uint32_t*>(scales), static_cast<T*>(y), n_rows,
+                      static_cast<int>(k), (k + 127) / 128);
 }
 
 }  // namespace

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
     *abort = 0;
     fence_mbar_init();
     // the first stages' loads, before the other warps are up
+    wait_for_earlier_kernels();
     for (; issued < min(n_loc, L::STAGES); ++issued) load_step(issued);
   }
   if (warp == 1) {
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
     tmem_dealloc(tmem, L::TMEM_COLS);
   }
   if (splits > 1) cluster_sync();
+  wait_for_earlier_kernels();
   // this block's share of the tile's tokens x 32 groups of four features
   const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), p.m - static_cast<int64_t>(m_tile) * NT));
   const int share = (tokens * 32 + splits - 1) >> p.log_splits;
@@ -373,7 +375,7 @@ __device__ __forceinline__ void wide_coords(const WideParams& w, int t, int& m_t
   n_tile = within / gm;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
+__global__ void __launch_bounds__(Wide::kThreads, 1)
     mx4_wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw,
                     const __grid_constant__ CUtensorMap tm_y, const WideParams w) {
@@ -422,6 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's barriers are there
+  wait_for_earlier_kernels();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -674,19 +677,8 @@ cudaError_t launch_narrow(const Mx4Args& g, cudaStream_t s) {
   p.log_splits = 0;
   while (splits < kMaxSplits && m_tiles * n_tiles * splits * 2 <= sms && steps >= splits * 2) splits *= 2, ++p.log_splits;
   if (m_tiles > 65535 || n_tiles * splits > INT_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::ALLOC;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, mx4_narrow_kernel<NT>, tw, ta, tsw, tsa, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(mx4_narrow_kernel<NT>, dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles)),
+                      L::kThreads, L::ALLOC, splits, s, tw, ta, tsw, tsa, p);
 }
 
 cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
@@ -735,8 +727,7 @@ cudaError_t launch_wide(const Mx4Args& g, cudaStream_t s) {
   w.tiles = w.m_tiles * w.n_tiles;
   w.group_m = 8;
   const int pairs = w.tiles < most ? w.tiles : most;
-  mx4_wide_kernel<<<2 * pairs, L::kThreads, L::ALLOC, s>>>(ta, tw, tsa, tsw, ty, w);
-  return cudaGetLastError();
+  return launch_early(mx4_wide_kernel, dim3(2 * pairs), L::kThreads, L::ALLOC, 2, s, ta, tw, tsa, tsw, ty, w);
 }
 
 }  // namespace

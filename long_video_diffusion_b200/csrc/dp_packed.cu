@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
                                                                  int group, float scale, int causal) {
   using L = F32Lay<HD, RPW>;
+  wait_for_earlier_kernels();
   constexpr int kRows = L::kRows;
   extern __shared__ __align__(16) float smem[];
   constexpr int C = HD / 32;  // output columns per lane
@@ -234,10 +235,10 @@ cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  packed_f32_kernel<HD, RPW, N><<<dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, st>>>(
-      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
-      Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, a.n_heads, a.n_heads / a.n_kv_heads, a.softmax_scale, a.causal);
-  return cudaGetLastError();
+  return launch_early(packed_f32_kernel<HD, RPW, N>, dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, 1, st,
+                      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),
+                      static_cast<float*>(a.out), a.lse, Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, static_cast<int>(a.n_heads),
+                      static_cast<int>(a.n_heads / a.n_kv_heads), a.softmax_scale, static_cast<int>(a.causal));
 }
 
 // Four rows per warp, 32 per block; two while those blocks do not even fill the SMs once (single

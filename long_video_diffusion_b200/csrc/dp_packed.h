@@ -135,19 +135,7 @@ template <typename K, typename... A>
 cudaError_t launch_items(K kernel, const Cut& cut, int64_t items, int threads, int smem, cudaStream_t s, const A&... args) {
   const int64_t grid = (cut.items + (items - cut.items + cut.cluster - 1) / cut.cluster) * cut.cluster;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cut.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cut.cluster > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, cut.cluster, s, args...);
 }
 
 // The kernels for bf16 and f16: few rows (at most kFewRows of a sequence under one k/v head,

@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tma_load_2d(sb + s * L::STAGE + (L::CHUNKS + c) * L::CHUNK, &tm_v, kv * HD + c * 64, row, full(s));
     }
   };
+  wait_for_earlier_kernels();
   // the first stages' loads, before the others are up
   int issued = 0;
   if (warp == kWarps && lane == 0)

@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     }
     __syncwarp();
   };
+  wait_for_earlier_kernels();
   if (warp == L::W_PROD) {
     // the first item and its first loads, before the other warps are up
     w = decode<BN>(seqs, p, ip.item, ip.rank, ip.log_parts);

@@ -178,6 +178,35 @@ def test_captured_and_replayed_with_new_inputs(dp, m):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("m,k,n", [(3, 1536, 512), (700, 2080, 4360), (9000, 512, 64)])
+def test_calls_one_behind_the_other_on_the_same_buffers(dp, m, k, n):
+    """Kernels may start before the ones ahead of them have ended: results are those of a stream
+    that is waited for after every call, other libraries' kernels between them included."""
+    w = _quantize(dp, _rows(n, k, torch.bfloat16, 1).cuda())
+    x = _rows(m, k, torch.bfloat16, 2).cuda()
+    codes, scales = dp.mx4_empty(m, k)
+    y = torch.empty(m, n, device="cuda")
+    back = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+
+    def run(wait):
+        x.copy_(_rows(m, k, torch.bfloat16, 2))
+        seen = []
+        for i in range(12):
+            for call in (lambda: dp.mx4_quantize(x, codes, scales), lambda: dp.mx4_linear(codes, scales, *w, None, y),
+                         lambda: dp.mx4_dequantize(codes, scales, back), lambda: dp.mx4_quantize(back, codes, scales),
+                         lambda: dp.mx4_dequantize(codes, scales, back)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            seen += [y.clone(), back.clone()]
+            x.mul_(1.25)
+            x.add_(back, alpha=-0.5)
+        torch.cuda.synchronize()
+        return seen
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
 def test_first_call_of_a_thread(dp):
     """A thread that has made no CUDA call yet."""
     import threading

@@ -206,6 +206,30 @@ def test_more_items_than_blocks_fit(dp, d, causal):
     assert torch.equal(out[:sum(lens)], again[:sum(lens)])
 
 
+@pytest.mark.parametrize("q_lens,k_lens", [([1] * 9, [700, 3000, 5, 64, 1, 2000, 4100, 0, 129]), ([300, 40, 777], [300, 900, 777])])
+def test_calls_one_behind_the_other_on_the_same_buffers(dp, q_lens, k_lens):
+    """The output of one call is the query of the next, and its keys change between calls."""
+    for d, dtype in ((64, F16), (128, BF16), (128, F32)):
+        q, k, v = (t.cuda() for t in _inputs(q_lens, k_lens, 8, 2, d, dtype, spare=0))
+        a, b = q.clone(), torch.empty_like(q)
+
+        def run(wait):
+            a.copy_(q)
+            kk, seen = k.clone(), []
+            for i in range(10):
+                for src, dst in ((a, b), (b, a)):
+                    dp.packed_attention(src, kk, v, q_lens, k_lens, dst)
+                    if wait:
+                        torch.cuda.synchronize()
+                kk.mul_(-0.9)
+                a.add_(q)
+                seen.append(a.clone())
+            torch.cuda.synchronize()
+            return seen
+        for x, y in zip(run(True), run(False)):
+            assert torch.equal(x, y)
+
+
 def test_calls_of_two_threads(dp):
     """Two threads, a stream each, several calls under way: no call depends on another."""
     import threading
