@@ -516,8 +516,9 @@ dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, cons
  * of dt, rows ld_* elements apart (so that they may be column ranges of one buffer; multiples
  * of 16 bytes, at most 2^28 elements); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
  * sequence are neither read nor written, key rows of no sequence affect nothing, whatever they
- * hold.  The rows of a sequence have to be finite: a value that the causal mask hides takes
- * part in a product with weight 0.
+ * hold.  A sequence's values have to be finite: one that the causal mask hides takes part in a
+ * product with weight 0.  (A key that is hidden may hold anything.)  A query with a score that is
+ * NaN or +infinity, or none above -infinity, gets out = NaN.
  * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32)
  * or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
  * <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative length or start, n_seqs outside

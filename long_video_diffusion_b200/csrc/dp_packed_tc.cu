@@ -57,6 +57,7 @@ constexpr float kC0 = 0.9999992847442627f, kC1 = 0.6931217908859253f, kC2 = 0.24
 constexpr float kC3 = 0.05591785907745361f, kC4 = 0.009570102207362652f;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 constexpr float kMinX = -125.0f;
+constexpr float kLost = 1e30f;  // no row sum reaches this
 constexpr uint32_t kPolyMask = 0x1111u;  // column pairs of each 16 that use it
 
 constexpr int NQ = 2;            // query tiles per block
@@ -162,6 +163,13 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t a) {
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+// The larger, NaN if either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 template <int BN, int N>
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
             float x0, x1, a, b;
             f32x2_split(x, x0, x1);
             if ((kPolyMask >> c) & 1u) {
-              const uint64_t xc = f32x2(fmaxf(x0, kMinX), fmaxf(x1, kMinX));
+              const uint64_t xc = f32x2(max_nan(x0, kMinX), max_nan(x1, kMinX));
               const uint64_t r = fadd2(xc, magic2);
               const uint64_t f = ffma2(fadd2(r, nmagic2), neg1_2, xc);
               uint64_t q = ffma2(c4_2, f, c3_2);
@@ -748,6 +756,9 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
         float a0, a1;
         f32x2_split(fadd2(acc0, acc1), a0, a1);
         l_sum += a0 + a1;
+        // A NaN score (or infinity - infinity) is a weight of NaN, or 3.4e38 by the polynomial's integer
+        // addition; true sums stay below 2^8 times 2^31 keys.  From here on the row is NaN.
+        if (!(l_sum < kLost)) l_sum = NAN;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full(g));
@@ -771,7 +782,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
         // group's last heads) the lanes of a row store it themselves.
         // The warpgroup goes by one thread's view, so that it leaves together if the block gives up.
         int what = 0;
-        const float inv_l = sees ? 1.0f / l_sum : 0.0f;
+        const float inv_l = !sees ? 0.0f : m_ref == -INFINITY ? NAN : 1.0f / l_sum;  // (all its scores -inf: NaN)
         if (ok && p.lse && row_ok) p.lse[q_row * p.n_heads + head] = sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < L::KCH; ++c) {
@@ -844,7 +855,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
             }
           }
           // a part in which the row saw nothing: weight 0, its O (unwritten, or a product of zeros) unread
-          reinterpret_cast<float2*>(smem + L::OFF_ML)[g * BM + t] = make_float2(my_nt > 0 ? m_ref : -INFINITY, l_sum);
+          reinterpret_cast<float2*>(smem + L::OFF_ML)[g * BM + t] = make_float2(my_nt > 0 ? (l_sum < kLost ? m_ref : NAN) : -INFINITY, l_sum);
         }
         break;
       }
@@ -862,7 +873,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     cluster_sync();
     // block `rank` joins the rows r = rank, rank + splits, ...: four columns per thread
     volatile Work* wk = work_at(0);
-    const int tok0 = wk->tok0, head0 = wk->head0, heads = wk->heads, q_len = wk->q_len, first_q = wk->first_q;
+    const int tok0 = wk->tok0, head0 = wk->head0, heads = wk->heads, q_len = wk->q_len, k_len = wk->k_len, first_q = wk->first_q;
     const int n_rows = tok0 + p.tokens < q_len ? NQ * BM : BM;
     const int n_mine = (n_rows - ip.rank + splits - 1) >> ip.log_parts;
     for (int i = threadIdx.x; i < n_mine * (HD / 4); i += L::kThreads) {
@@ -895,7 +906,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
           a.z = fmaf(w, o[s].z, a.z);
           a.w = fmaf(w, o[s].w, a.w);
         }
-      const bool sees = top != -INFINITY;
+      const bool sees = min(k_len, keys_seen(tok, q_len, k_len, p.causal)) > 0;
       const float inv = sees ? 1.0f / l : 0.0f;
       const int64_t at = first_q + static_cast<int64_t>(tok);
       *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =

@@ -180,6 +180,58 @@ def test_another_sequence_does_not_matter(dp):
         assert torch.equal(got[:100], ref[:100]) and torch.equal(got[170:300], ref[170:300])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("q_len,k_len,n", [(1, 200, 70), (3, 64, 64), (40, 70, 70), (150, 600, 9), (70, 3000, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_values_show(dp, d, q_len, k_len, n, dtype):
+    """Sequence i's key at about i k_len / n is spoilt: the queries that see it get NaN, those that do
+    not what they get without it; a spoilt query likewise."""
+    heads, group = 4, 2
+    q_lens, k_lens = [q_len] * n, [k_len] * n
+    q, k, v = _inputs(q_lens, k_lens, heads, heads // group, d, dtype, spare=0)
+    clean, clean_lse = (torch.empty(q.shape, dtype=dtype, device="cuda"), torch.empty(q.shape[:2], device="cuda"))
+    dp.packed_attention(q.cuda(), k.cuda(), v.cuda(), q_lens, k_lens, clean, lse=clean_lse)
+    places = [min(k_len - 1, max(0, k_len - n) // 2 + i if n >= 64 else i * k_len // n + 5) for i in range(n)]
+    for bad in (float("nan"), float("inf")):
+        k2, q2 = k.clone(), q.clone()
+        hit = torch.zeros(q.shape[:2], dtype=torch.bool)
+        for i, j in enumerate(places):
+            k2[i * k_len + j, 1, 3] = bad
+            for t in range(q_len):  # its queries are its last rows; the second k/v head's query heads
+                if j > k_len - q_len + t:
+                    continue
+                for h in (2, 3):
+                    # the score is bad * q[3] + finite: NaN, or an infinity of q[3]'s sign
+                    hit[i * q_len + t, h] = bad != bad or q[i * q_len + t, h, 3] >= 0
+        q2[q_len - 1, 0, 7] = float("nan")
+        hit[q_len - 1, 0] = True
+        out, lse = torch.empty_like(clean), torch.empty_like(clean_lse)
+        dp.packed_attention(q2.cuda(), k2.cuda(), v.cuda(), q_lens, k_lens, out, lse=lse)
+        assert torch.equal(torch.isnan(out).all(dim=2).cpu(), hit)
+        assert torch.equal(torch.isnan(out).any(dim=2).cpu(), hit)
+        assert torch.equal(torch.isnan(lse).cpu(), hit)
+        # a score of -infinity is a weight of 0: not the clean result, the others are
+        same = torch.ones(q.shape[:2], dtype=torch.bool)
+        for i, j in enumerate(places):
+            for t in range(q_len):
+                if j <= k_len - q_len + t:
+                    same[i * q_len + t, 2:] = False
+        same[q_len - 1, 0] = False
+        assert torch.equal(out.cpu()[same], clean.cpu()[same]) and torch.equal(lse.cpu()[same], clean_lse.cpu()[same])
+
+
+def test_no_score_above_minus_infinity(dp):
+    for q_lens, k_lens in (([1], [40]), ([1], [9000]), ([30], [60]), ([200], [5000])):
+        for dtype in (BF16, F16, F32):
+            for d in (64, 128):
+                q, k, v = _inputs(q_lens, k_lens, 2, 1, d, dtype, spare=0)
+                q[:, 0, 0], k[:, 0, 0] = 1.0, -float("inf")
+                q[:, 1, 0] = -1.0  # and these scores +infinity
+                out = torch.empty(q.shape, dtype=dtype, device="cuda")
+                dp.packed_attention(q.cuda(), k.cuda(), v.cuda(), q_lens, k_lens, out, causal=False)
+                assert torch.isnan(out).all()
+
+
 @pytest.mark.parametrize("n", [33, 1000, 1024])
 def test_many_sequences(dp, n):
     rng = np.random.default_rng(n)
