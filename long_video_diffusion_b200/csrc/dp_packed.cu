@@ -266,11 +266,45 @@ cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t s) {
   if (a.n_seqs < 1 || a.n_seqs > DP_MAX_SEQS || (a.head_dim != 64 && a.head_dim != 128)) return cudaErrorInvalidValue;
   if (a.dt == DP_F32) return launch_f32(a, s);
-  // few rows: bound by reading the keys, which the kernel for few rows does at twice the rate
+  // Sequences with few rows go to the kernel for few rows, which reads their keys at twice the rate
+  // (eight tokens over 1 to 8191 keys: 27 us, 66 with the other).  Beside longer ones a launch of
+  // their own has to pay: it does from about 40 tiles of 64 keys per SM on.  Measured, us, one launch
+  // | two, 32 heads on 8 k/v heads of 128, a chunk of 512 tokens and single tokens: 8 over 4000 keys
+  // (27 tiles per SM) 36.6 | 40.1; 64 over 1000 (55) 68 | 60; 31 over 4000 (105) 163 | 123; 200 over
+  // 2000 (346) 325 | 274; 16 k/v heads of 64, 8 over 4000 (54) 44.7 | 35.3, 64 over 1000 (110) 115 | 57.
   const int group = a.n_heads / a.n_kv_heads;
-  bool few = true;
-  for (int i = 0; i < a.n_seqs; ++i) few = few && static_cast<int64_t>(a.q_len[i]) * group <= kFewRows;
-  return few ? launch_packed_few(a, s) : launch_packed_tc(a, s);
+  auto is_few = [&](int i) { return static_cast<int64_t>(a.q_len[i]) * group <= kFewRows; };
+  int n_few = 0;
+  int64_t tiles = 0;  // of the keys of the sequences with few rows
+  for (int i = 0; i < a.n_seqs; ++i)
+    if (is_few(i)) {
+      ++n_few;
+      tiles += (static_cast<int64_t>(a.k_len[i]) + 63) / 64;
+    }
+  if (n_few == a.n_seqs) return launch_packed_few(a, s);
+  int dev = 0, sms = 148;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  if (tiles * a.n_kv_heads < 40 * static_cast<int64_t>(sms)) return launch_packed_tc(a, s);
+  int32_t first_q[DP_MAX_SEQS], q_len[DP_MAX_SEQS], first_k[DP_MAX_SEQS], k_len[DP_MAX_SEQS];
+  for (int few = 0; few < 2; ++few) {
+    PackedArgs part = a;
+    part.n_seqs = 0;
+    for (int i = 0; i < a.n_seqs; ++i)
+      if (is_few(i) == (few == 1)) {
+        first_q[part.n_seqs] = a.first_q[i];
+        q_len[part.n_seqs] = a.q_len[i];
+        first_k[part.n_seqs] = a.first_k[i];
+        k_len[part.n_seqs++] = a.k_len[i];
+      }
+    part.first_q = first_q;
+    part.q_len = q_len;
+    part.first_k = first_k;
+    part.k_len = k_len;
+    e = few ? launch_packed_few(part, s) : launch_packed_tc(part, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace dp

@@ -232,6 +232,23 @@ def test_no_score_above_minus_infinity(dp):
                 assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("n,heads,kv_heads,keys,d", [(3, 8, 8, 2000, 64), (12, 16, 16, 2100, 64), (40, 8, 4, 2500, 128)])
+def test_tokens_beside_prompts(dp, n, heads, kv_heads, keys, d, tokens):
+    """Single tokens and drafts over a cache in one call with chunks of prompts, in any order, few
+    enough keys to be taken along and enough for a launch of their own."""
+    rng = np.random.default_rng(n)
+    k_lens = [int(x) for x in rng.integers(keys // 2, keys + keys // 2, n)]
+    q_lens = [tokens] * n
+    for at, ql, kl in ((0, 140, 300), (n // 2, 0, 70), (n, 65, 65), (n + 3, 20, 5)):
+        q_lens.insert(at, ql)
+        k_lens.insert(at, kl)
+    for dtype in (BF16, F16):
+        q, k, v = _inputs(q_lens, k_lens, heads, kv_heads, d, dtype)
+        out, lse = _run(dp, q, k, v, q_lens, k_lens)
+        _check(out, lse, q, k, v, q_lens, k_lens, None, True)
+
+
 @pytest.mark.parametrize("n", [33, 1000, 1024])
 def test_many_sequences(dp, n):
     rng = np.random.default_rng(n)
