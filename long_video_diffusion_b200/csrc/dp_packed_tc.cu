@@ -31,6 +31,11 @@
 // A tile of keys that ends behind its sequence holds other rows: their scores are masked, and
 // the producer warp writes zeros over their V rows before the product reads them (0 * NaN).
 // Every wait is bounded (dp_device.cuh).
+//
+// Bound by the softmax's issue slots and exponentials at head_dim 64, by the tensor cores and the
+// power limit at 128.  Causal 16384 tokens of 16 heads on 4: head_dim 128 900 to 1070 us (1.22 to 1.03
+// PFLOP/s as the clock falls under the limit), head_dim 64 708 us; nine prompts of 1 to 2048 tokens, 32
+// heads on 8 of 128: 111 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
