@@ -118,6 +118,35 @@ def test_linear_many_tiles(dp, m, n, k):
     _check_product(dp, m, n, k, True, torch.bfloat16)
 
 
+def test_offsets_behind_32_bits(dp):
+    """More than 2^32 elements quantised, read back and multiplied: the last rows are the oracle's."""
+    rows, k, n, last = 530000, 8192, 8200, 300
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    tail = _rows(last, k, torch.bfloat16, 5)
+    x[-last:] = tail.cuda()
+    codes, scales = _quantize(dp, x)
+    want, want_scales = O.mx4_quantize(tail.double().numpy())
+    assert np.array_equal(codes[-last:].cpu().numpy(), want)
+    back = x
+    dp.mx4_dequantize(codes, scales, back)
+    values = O.mx4_values(want, want_scales)
+    assert torch.equal(back[-last:].cpu().double(), torch.from_numpy(values)) and not bool(back[:1000].any())
+    del x, back
+    w = _rows(n, 64, torch.bfloat16, 6)
+    a = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    a[-last:] = _rows(last, 64, torch.bfloat16, 7).cuda()
+    qa, qw = _quantize(dp, a), _quantize(dp, w.cuda())
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    dp.mx4_linear(*qa, *qw, None, y)
+    dp.device_status()
+    va = O.mx4_values(*O.mx4_quantize(a[-last:].cpu().double().numpy()))
+    vw = O.mx4_values(*O.mx4_quantize(w.double().numpy()))
+    exact, size = va @ vw.T, np.abs(va) @ np.abs(vw).T
+    err = np.abs(y[-last:].cpu().double().numpy() - exact)
+    assert (err <= 2.0 ** -8 * np.abs(exact) + 65 * 2.0 ** -24 * 1.01 * size + 1e-30).all()
+    assert not bool(y[:1000].any())
+
+
 @pytest.mark.parametrize("m", [3, 700])
 def test_linear_nan_block_reaches_its_row_only(dp, m):
     """A block that was quantised from a NaN makes its row NaN and no other; a f16 output saturates."""

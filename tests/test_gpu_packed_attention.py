@@ -333,6 +333,30 @@ def test_long_sequence_last_rows(dp, dtype):
     _check(out[-150:], lse[-150:], q[-150:], k, v, [150], [n], None, True)
 
 
+@pytest.mark.parametrize("dtype,q_lens,k_lens", [
+    (BF16, [300, 1, 90], [300, 700, 1100]), (F16, [1, 3], [900, 1200]), (F32, [40, 1], [500, 300])])
+def test_offsets_behind_32_bits(dp, dtype, q_lens, k_lens):
+    """Rows 2^20 elements apart, the last sequences' behind 2^32 elements (fp32: 2^31)."""
+    heads, kv, d, pitch = 4, 2, 64, 1 << 20
+    rows = 4200 if dtype != F32 else 2300
+    starts = [0] * (len(k_lens) - 1) + [rows - k_lens[-1]]
+    q_all, k_all = list(q_lens), list(k_lens)
+    if sum(q_lens) > 40:  # an empty-handed sequence in front: its queries see no key
+        q_all, k_all, starts = [rows - sum(q_lens)] + q_all, [0] + k_all, [0] + starts
+    q, k, v = _inputs(q_all, k_all, heads, kv, d, dtype, k_starts=starts, spare=0)
+    nq = sum(q_all)
+    held, res = (torch.empty(rows, pitch, dtype=dtype, device="cuda") for _ in range(2))
+    parts = held[:, :(heads + 2 * kv) * d].unflatten(1, (-1, d))
+    parts[:nq, :heads].copy_(q)
+    parts[:, heads:].copy_(torch.cat([k, v], dim=1))
+    out = res[:nq, 256:256 + heads * d].unflatten(1, (-1, d))
+    lse = torch.empty(nq, heads, device="cuda")
+    dp.packed_attention(parts[:nq, :heads], parts[:, heads:heads + kv], parts[:, heads + kv:], q_all, k_all, out,
+                        k_starts=starts, lse=lse)
+    dp.device_status()
+    _check(out, lse, q, k, v, q_all, k_all, starts, True)
+
+
 def test_side_stream_and_two_captured_graphs(dp):
     lens = [1, 1, 40]
     k_lens = [900, 3000, 40]
