@@ -27,6 +27,10 @@ namespace dp {
 
 namespace {
 
+// f16 weights are taken 2^15 times as large, so that those under 2^-14 of the largest keep their
+// bits; sums and outputs carry the factor, which cancels.
+template <bool F16>
+constexpr float kWeightLog2 = F16 ? 15.0f : 0.0f;
 constexpr int kRows = 16;
 constexpr int kKeys = 64;     // per tile
 constexpr int kWarps = 4;     // of 16 keys each; one more loads
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         move |= mn != m[h];
         m[h] = mn;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e] - ref);
+        for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e] - (ref - kWeightLog2<F16>));
         l[h] = l[h] * f[h] + (x[0] + x[1]) + (x[2] + x[3]);
         pf[h] = pack2<F16>(x[0], x[1]);
         pf[h + 2] = pack2<F16>(x[2], x[3]);
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t at = first_q + static_cast<int64_t>(tok);
     *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-    if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + (log2f(l) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
   };
   for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
     const int row = i / (HD / 4), c = (i % (HD / 4)) * 4;

@@ -63,6 +63,10 @@ constexpr float kC3 = 0.05591785907745361f, kC4 = 0.009570102207362652f;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 constexpr float kMinX = -125.0f;
 constexpr float kLost = 1e30f;  // no row sum reaches this
+// f16 weights are taken 2^7 times as large (at most 2^15: the running maximum may lag by 2^8), so that
+// those under 2^-14 of the largest keep their bits; sum and O carry the factor, which cancels.
+template <bool F16>
+constexpr float kWeightLog2 = F16 ? 7.0f : 0.0f;
 constexpr uint32_t kPolyMask = 0x1111u;  // column pairs of each 16 that use it
 
 constexpr int NQ = 2;            // query tiles per block
@@ -699,7 +703,8 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
         }
         // a row that has seen no key yet has no maximum: all its scores are -inf, all its weights 0
         const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
-        const uint64_t nm2 = f32x2(-ref, -ref);
+        const float nm = kWeightLog2<F16> - ref;
+        const uint64_t nm2 = f32x2(nm, nm);
         const uint64_t magic2 = f32x2(kMagic, kMagic), nmagic2 = f32x2(-kMagic, -kMagic), neg1_2 = f32x2(-1.0f, -1.0f);
         const uint64_t c0_2 = f32x2(kC0, kC0), c1_2 = f32x2(kC1, kC1), c2_2 = f32x2(kC2, kC2);
         const uint64_t c3_2 = f32x2(kC3, kC3), c4_2 = f32x2(kC4, kC4);
@@ -788,7 +793,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
         // The warpgroup goes by one thread's view, so that it leaves together if the block gives up.
         int what = 0;
         const float inv_l = !sees ? 0.0f : m_ref == -INFINITY ? NAN : 1.0f / l_sum;  // (all its scores -inf: NaN)
-        if (ok && p.lse && row_ok) p.lse[q_row * p.n_heads + head] = sees ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+        if (ok && p.lse && row_ok) p.lse[q_row * p.n_heads + head] = sees ? (m_ref + (log2f(l_sum) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < L::KCH; ++c) {
           if (t == 0) {
@@ -916,7 +921,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
       const int64_t at = first_q + static_cast<int64_t>(tok);
       *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
           make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-      if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + (log2f(l) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
     }
     cluster_sync();  // no block leaves while another reads its shared memory
   }

@@ -142,6 +142,24 @@ def test_flat_and_peaked_softmax(dp, dtype, std):
     _check(out, lse, q, k, v, lens, lens, None, True)
 
 
+@pytest.mark.parametrize("q_lens,k_lens", [([1], [200]), ([1, 1], [4000, 300]), ([90], [700]), ([20], [5000])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_weights_keep_their_bits(dp, d, q_lens, k_lens):
+    """One key has all but some 2^-15 of the weight and a value of 0 in half the columns, where the
+    output is what the other keys' small weights give: f16 ones under 2^-14 would lose bits."""
+    for dtype in (F16, BF16, F32):
+        q, k, v = _inputs(q_lens, k_lens, 4, 2, d, dtype, spare=0, std=0.2)
+        q[:, :, 0] = 1.0
+        k[:, :, 0] = 0.0
+        at = 0
+        for n in k_lens:
+            k[at + n // 2, :, 0] = 15 * float(np.log(2)) + float(np.log(n))  # 2^15 times all the others
+            v[at + n // 2, :, ::2] = 0.0
+            at += n
+        out, lse = _run(dp, q, k, v, q_lens, k_lens, causal=False, scale=1.0)
+        _check(out, lse, q, k, v, q_lens, k_lens, None, False, scale=1.0)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_scores_that_grow_and_fall_along_the_keys(dp, dtype):
     """The running maximum moves at every tile of keys (growing) or never after the first."""
