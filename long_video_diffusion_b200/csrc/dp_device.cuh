@@ -49,7 +49,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Programmatic dependent launch.  A kernel launched so may start before the kernels before it in
-// the stream have ended; it waits here before it touches any memory of the caller's.
+// the stream have ended; it waits here before it touches any memory of the caller's, and before it
+// takes tensor memory (which a block of theirs on the same SM may still have to take).
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The next kernel's blocks may come as soon as all of this one's have got here (they wait as above).

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads)
     for (; issued < min(n_loc, L::STAGES); ++issued) load_step(issued);
   }
   if (warp == 1) {
+    wait_for_earlier_kernels();
     tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
+    wait_for_earlier_kernels();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }

@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == L::W_ISS) {
+    wait_for_earlier_kernels();
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
