@@ -84,6 +84,11 @@ struct Strides {
   int64_t q, k, v, out;
 };
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 // A warp's RPW rows against a tile of 64 keys: a lane holds two keys' scores of each row, then,
 // with the weights in shared memory, HD / 32 columns of each row's output.  Either way a 16-byte
 // read from shared memory feeds two to four multiply-adds per lane.
@@ -131,54 +136,60 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = 0.0f;
   }
+  // 64 rows of k (or v) into shared memory; rows behind the sequence count as zeros, whatever they hold
+  auto load = [&](const float* src, int64_t pitch, float* dst, int dst_pitch, int j0) {
+    constexpr int kStep = 32 * kWarps / (HD / 4);
+    const int c = (threadIdx.x % (HD / 4)) * 4;
+    int j = threadIdx.x / (HD / 4);
+    const float* p = src + (seqs.first_k[s] + static_cast<int64_t>(j0 + j)) * pitch + kv * HD + c;
+#pragma unroll
+    for (; j < kKeys; j += kStep, p += kStep * pitch) copy16(dst + j * dst_pitch + c, j0 + j < k_len ? p : src, j0 + j < k_len);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // V comes while the scores are taken, the next K while the products with V are
+  if (seen > 0) load(k, ld.k, sk, L::KP, 0);
   for (int j0 = 0; j0 < seen; j0 += kKeys) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * (HD / 4); i += 32 * kWarps) {
-      const int j = i / (HD / 4), c = (i % (HD / 4)) * 4;
-      float4 x = make_float4(0, 0, 0, 0), y = x;
-      if (j0 + j < k_len) {  // rows behind the sequence count as zeros, whatever they hold
-        const int64_t row = seqs.first_k[s] + static_cast<int64_t>(j0 + j);
-        x = *reinterpret_cast<const float4*>(k + row * ld.k + kv * HD + c);
-        y = *reinterpret_cast<const float4*>(v + row * ld.v + kv * HD + c);
-      }
-      *reinterpret_cast<float4*>(sk + j * L::KP + c) = x;
-      *reinterpret_cast<float4*>(sv + j * HD + c) = y;
-    }
-    __syncthreads();
-    if (warp * RPW >= n_rows) continue;
-    float dot[RPW][2] = {};
-    const float* k0 = sk + lane * L::KP;
-    const float* qr = sq + warp * RPW * HD;
+    load(v, ld.v, sv, HD, j0);
+    if (warp * RPW < n_rows) {
+      float dot[RPW][2] = {};
+      const float* k0 = sk + lane * L::KP;
+      const float* qr = sq + warp * RPW * HD;
 #pragma unroll 2
-    for (int c = 0; c < HD; c += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(k0 + c);
-      const float4 z = *reinterpret_cast<const float4*>(k0 + 32 * L::KP + c);
+      for (int c = 0; c < HD; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(k0 + c);
+        const float4 z = *reinterpret_cast<const float4*>(k0 + 32 * L::KP + c);
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+          const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
+          dot[r][0] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r][0]))));
+          dot[r][1] = fmaf(z.x, y.x, fmaf(z.y, y.y, fmaf(z.z, y.z, fmaf(z.w, y.w, dot[r][1]))));
+        }
+      }
 #pragma unroll
       for (int r = 0; r < RPW; ++r) {
-        const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
-        dot[r][0] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r][0]))));
-        dot[r][1] = fmaf(z.x, y.x, fmaf(z.y, y.y, fmaf(z.z, y.z, fmaf(z.w, y.w, dot[r][1]))));
+        const float x0 = j0 + lane < lim[r] ? dot[r][0] : -INFINITY;
+        const float x1 = j0 + 32 + lane < lim[r] ? dot[r][1] : -INFINITY;
+        float t = fmaxf(x0, x1);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        const float mn = fmaxf(m[r], t);
+        const float ref = mn == -INFINITY ? 0.0f : mn;  // a row that has seen no key: weights 0
+        const float f = expf(m[r] - ref);
+        const float p0 = expf(x0 - ref), p1 = expf(x1 - ref);
+        m[r] = mn;
+        l[r] = l[r] * f + (p0 + p1);
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[r][c] *= f;
+        sp[r * L::PP + lane] = p0;
+        sp[r * L::PP + 32 + lane] = p1;
       }
     }
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-      const float x0 = j0 + lane < lim[r] ? dot[r][0] : -INFINITY;
-      const float x1 = j0 + 32 + lane < lim[r] ? dot[r][1] : -INFINITY;
-      float t = fmaxf(x0, x1);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-      const float mn = fmaxf(m[r], t);
-      const float ref = mn == -INFINITY ? 0.0f : mn;  // a row that has seen no key: weights 0
-      const float f = expf(m[r] - ref);
-      const float p0 = expf(x0 - ref), p1 = expf(x1 - ref);
-      m[r] = mn;
-      l[r] = l[r] * f + (p0 + p1);
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[r][c] *= f;
-      sp[r * L::PP + lane] = p0;
-      sp[r * L::PP + 32 + lane] = p1;
-    }
-    __syncwarp();
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (j0 + kKeys < seen) load(k, ld.k, sk, L::KP, j0 + kKeys);
+    if (warp * RPW >= n_rows) continue;
     const int n_keys = min(kKeys, seen - j0);
 #pragma unroll 1
     for (int j = 0; j < n_keys; j += 4) {  // (rows behind the sequence are zeros, weights behind `seen` too)
@@ -199,7 +210,6 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
           acc[r][c] = fmaf(p.x, y[0][c], fmaf(p.y, y[1][c], fmaf(p.z, y[2][c], fmaf(p.w, y[3][c], acc[r][c]))));
       }
     }
-    __syncwarp();
   }
 #pragma unroll
   for (int r = 0; r < RPW; ++r) {
