@@ -67,6 +67,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kKeys = 64;  // keys per tile: two per lane
+// key tiles that a block's start and end cost, and those of a block that joins parts
+constexpr int kF32Whole = 1, kF32Part = 2;
 
 // RPW: query rows per warp.
 template <int HD, int RPW>
@@ -84,6 +86,25 @@ struct Strides {
   int64_t q, k, v, out;
 };
 
+// Items, (row tile, k/v head), whose keys a cluster's blocks share: the first n_cut.
+struct F32Items {
+  FastDiv by_kv;
+  int32_t n_kv, log_cluster, n_cut, n_items;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 16 bytes of block `rank`'s shared memory.
+__device__ __forceinline__ float4 ld_peer4(const float* at, int rank) {
+  uint32_t a;
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 // 16 bytes to shared memory, or zeros.
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -97,8 +118,11 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
                                                                  const float* __restrict__ v, float* __restrict__ out,
                                                                  float* __restrict__ lse, Strides ld,
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
-                                                                 int group, float scale, int causal) {
+                                                                 int group, float scale, int causal, F32Items items) {
   using L = F32Lay<HD, RPW>;
+  const ItemPart ip = item_part(items.log_cluster, items.n_cut);
+  if (ip.item >= items.n_items) return;  // behind the last item: its cluster never joins
+  const int parts = 1 << ip.log_parts;
   wait_for_earlier_kernels();
   constexpr int kRows = L::kRows;
   extern __shared__ __align__(16) float smem[];
@@ -108,7 +132,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
   float* sq = smem + L::OFF_Q;  // [kRows][HD], scaled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* sp = smem + L::OFF_P + warp * RPW * L::PP;
-  const int tile = blockIdx.x, kv = blockIdx.y;
+  const int tile = items.by_kv.div(ip.item), kv = ip.item - tile * items.n_kv;
   const int s = seq_of_tile(seqs, tile);
   const int q_len = seqs.q_len[s], k_len = seqs.k_len[s];
   const int rows = q_len * group;
@@ -147,8 +171,10 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // V comes while the scores are taken, the next K while the products with V are
-  if (seen > 0) load(k, ld.k, sk, L::KP, 0);
-  for (int j0 = 0; j0 < seen; j0 += kKeys) {
+  const int per = ((seen + kKeys - 1) / kKeys + parts - 1) >> ip.log_parts;  // key tiles of a part
+  const int begin = ip.rank * per * kKeys, end = min(seen, begin + per * kKeys);
+  if (begin < end) load(k, ld.k, sk, L::KP, begin);
+  for (int j0 = begin; j0 < end; j0 += kKeys) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     load(v, ld.v, sv, HD, j0);
@@ -188,7 +214,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    if (j0 + kKeys < seen) load(k, ld.k, sk, L::KP, j0 + kKeys);
+    if (j0 + kKeys < end) load(k, ld.k, sk, L::KP, j0 + kKeys);
     if (warp * RPW >= n_rows) continue;
     const int n_keys = min(kKeys, seen - j0);
 #pragma unroll 1
@@ -211,29 +237,61 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
       }
     }
   }
+  auto store = [&](int row, int c, float4 a, float top, float sum, bool sees) {
+    const int64_t tok = seqs.first_q[s] + static_cast<int64_t>(row / group);
+    const int h = kv * group + row % group;
+    const float inv = 1.0f / sum;
+    *reinterpret_cast<float4*>(out + tok * ld.out + h * HD + c) =
+        sees ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0, 0, 0, 0);
+    if (lse && c == 0) lse[tok * n_heads + h] = sees ? top + logf(sum) : -INFINITY;
+  };
+  // the rows' results through shared memory (over K: every warp has left the scores): [row][HD], then
+  // (maximum, sum)
+  float* sums = sk;
+  float* sml = sk + kRows * HD;
+  static_assert(kRows * (HD + 4) <= kKeys * L::KP, "the results fit over K");
 #pragma unroll
   for (int r = 0; r < RPW; ++r) {
-    const int row = row0 + warp * RPW + r;
-    if (row >= rows) break;
     float sum = l[r];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int64_t tok = seqs.first_q[s] + static_cast<int64_t>(row / group);
-    const int h = kv * group + row % group;
-    const float inv = lim[r] > 0 ? 1.0f / sum : 0.0f;
+    const int row = warp * RPW + r;
 #pragma unroll
-    for (int c = 0; c < C; c += 2)
-      *reinterpret_cast<float2*>(out + tok * ld.out + h * HD + lane * C + c) =
-          lim[r] > 0 ? make_float2(acc[r][c] * inv, acc[r][c + 1] * inv) : make_float2(0.0f, 0.0f);
-    if (lse && lane == 0) lse[tok * n_heads + h] = lim[r] > 0 ? m[r] + logf(sum) : -INFINITY;
+    for (int c = 0; c < C; c += 2) *reinterpret_cast<float2*>(sums + row * HD + lane * C + c) = make_float2(acc[r][c], acc[r][c + 1]);
+    if (lane == 0) *reinterpret_cast<float4*>(sml + row * 4) = make_float4(m[r], sum, 0.0f, 0.0f);
   }
+  __syncthreads();
+  if (parts > 1) cluster_sync();
+  // block `rank` joins the rows rank, rank + parts, ...
+  for (int i = threadIdx.x; i < ((n_rows - ip.rank + parts - 1) >> ip.log_parts) * (HD / 4); i += 32 * kWarps) {
+    const int row = ip.rank + (i / (HD / 4)) * parts, c = (i % (HD / 4)) * 4;
+    const bool sees = min(k_len, keys_seen((row0 + row) / group, q_len, k_len, causal)) > 0;
+    if (parts == 1) {
+      store(row0 + row, c, *reinterpret_cast<const float4*>(sums + row * HD + c), sml[row * 4], sml[row * 4 + 1], sees);
+    } else {
+      float top = -INFINITY, sum = 0.0f;
+      for (int t = 0; t < parts; ++t) top = fmaxf(top, ld_peer4(sml + row * 4, t).x);
+      float4 a = make_float4(0, 0, 0, 0);
+      for (int t = 0; t < parts; ++t) {
+        const float4 ml = ld_peer4(sml + row * 4, t), x = ld_peer4(sums + row * HD + c, t);
+        const float w = ml.x == -INFINITY ? 0.0f : expf(ml.x - top);
+        sum = fmaf(w, ml.y, sum);
+        a.x = fmaf(w, x.x, a.x);
+        a.y = fmaf(w, x.y, a.y);
+        a.z = fmaf(w, x.z, a.z);
+        a.w = fmaf(w, x.w, a.w);
+      }
+      store(row0 + row, c, a, top, sum, sees);
+    }
+  }
+  if (parts > 1) cluster_sync();  // no block leaves while another reads its shared memory
 }
 
 template <int HD, int RPW, int N>
-cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
+cudaError_t launch_rows(const PackedArgs& a, int sms, cudaStream_t st) {
   PackedSeqs<N> s;
   const int64_t tiles = plan_packed(a, a.n_heads / a.n_kv_heads, F32Lay<HD, RPW>::kRows, s);
-  if (tiles < 0 || a.n_kv_heads > 65535) return cudaErrorInvalidValue;
+  if (tiles < 0 || tiles * a.n_kv_heads > INT_MAX) return cudaErrorInvalidValue;
   constexpr int bytes = F32Lay<HD, RPW>::FLOATS * 4;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -245,10 +303,13 @@ cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  return launch_early(packed_f32_kernel<HD, RPW, N>, dim3(static_cast<unsigned>(tiles), a.n_kv_heads), 32 * kWarps, bytes, 1, st,
-                      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),
-                      static_cast<float*>(a.out), a.lse, Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, static_cast<int>(a.n_heads),
-                      static_cast<int>(a.n_heads / a.n_kv_heads), a.softmax_scale, static_cast<int>(a.causal));
+  const int64_t n_items = tiles * a.n_kv_heads;
+  const Cut cut = choose_cut(a.causal, s, a.n_kv_heads, kKeys, (HD == 64 ? 4 : 2) * sms, kF32Whole, kF32Part, kMaxCluster);
+  const F32Items items = {fast_div(a.n_kv_heads), a.n_kv_heads, cut.log_cluster(), static_cast<int32_t>(cut.items), static_cast<int32_t>(n_items)};
+  return launch_items(packed_f32_kernel<HD, RPW, N>, cut, n_items, 32 * kWarps, bytes, st, static_cast<const float*>(a.q),
+                      static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
+                      Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, static_cast<int>(a.n_heads),
+                      static_cast<int>(a.n_heads / a.n_kv_heads), a.softmax_scale, static_cast<int>(a.causal), items);
 }
 
 // Four rows per warp, 32 per block; two while those blocks do not even fill the SMs once (single
@@ -263,7 +324,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   int64_t blocks = 0;
   for (int i = 0; i < a.n_seqs; ++i)
     blocks += (static_cast<int64_t>(a.q_len[i]) * (a.n_heads / a.n_kv_heads) + 31) / 32 * a.n_kv_heads;
-  return blocks >= sms ? launch_rows<HD, 4, N>(a, st) : launch_rows<HD, 2, N>(a, st);
+  return blocks >= sms ? launch_rows<HD, 4, N>(a, sms, st) : launch_rows<HD, 2, N>(a, sms, st);
 }
 
 cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
