@@ -65,7 +65,6 @@ cudaError_t device_and_sms(int* dev, int* sms) {
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kKeys = 64;  // keys per tile: two per lane
 // key tiles that a block's start and end cost, and those of a block that joins parts
 constexpr int kF32Whole = 1, kF32Part = 2;
@@ -73,13 +72,13 @@ constexpr int kF32Whole = 1, kF32Part = 2;
 // RPW: query rows per warp.
 template <int HD, int RPW>
 struct F32Lay {
+  static constexpr int kWarps = RPW == 8 ? 4 : 8;
   static constexpr int kRows = kWarps * RPW;  // per block
   static constexpr int KP = HD + 4;       // pitch of a key row: 16-byte reads of 32 rows without conflicts
-  static constexpr int PP = kKeys + 4;    // pitch of a row of weights
   static constexpr int OFF_V = kKeys * KP;
   static constexpr int OFF_Q = OFF_V + kKeys * HD;
   static constexpr int OFF_P = OFF_Q + kRows * HD;
-  static constexpr int FLOATS = OFF_P + kRows * PP;
+  static constexpr int FLOATS = OFF_P + kRows * kKeys;  // weights: [two rows][key][row]
 };
 
 struct Strides {
@@ -114,7 +113,7 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
 // with the weights in shared memory, HD / 32 columns of each row's output.  Either way a 16-byte
 // read from shared memory feeds two to four multiply-adds per lane.
 template <int HD, int RPW, int N>
-__global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
+__global__ void __launch_bounds__(32 * F32Lay<HD, RPW>::kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                                  const float* __restrict__ v, float* __restrict__ out,
                                                                  float* __restrict__ lse, Strides ld,
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
@@ -124,14 +123,14 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
   if (ip.item >= items.n_items) return;  // behind the last item: its cluster never joins
   const int parts = 1 << ip.log_parts;
   wait_for_earlier_kernels();
-  constexpr int kRows = L::kRows;
+  constexpr int kRows = L::kRows, kWarps = L::kWarps;
   extern __shared__ __align__(16) float smem[];
   constexpr int C = HD / 32;  // output columns per lane
   float* sk = smem;           // [kKeys][KP]
   float* sv = smem + L::OFF_V;
   float* sq = smem + L::OFF_Q;  // [kRows][HD], scaled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* sp = smem + L::OFF_P + warp * RPW * L::PP;
+  float* sp = smem + L::OFF_P + warp * RPW * kKeys;
   const int tile = items.by_kv.div(ip.item), kv = ip.item - tile * items.n_kv;
   const int s = seq_of_tile(seqs, tile);
   const int q_len = seqs.q_len[s], k_len = seqs.k_len[s];
@@ -150,7 +149,8 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     *reinterpret_cast<float4*>(sq + r * HD + c) = make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
   }
   int lim[RPW];
-  float m[RPW], l[RPW], acc[RPW][C];  // l: this lane's keys
+  float m[RPW], l[RPW];      // l: this lane's keys
+  uint64_t acc[RPW / 2][C];  // of two rows each
 #pragma unroll
   for (int r = 0; r < RPW; ++r) {
     const int row = row0 + warp * RPW + r;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     m[r] = -INFINITY;
     l[r] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[r][c] = 0.0f;
+    for (int c = 0; c < C; ++c) acc[r / 2][c] = 0;
   }
   // 64 rows of k (or v) into shared memory; rows behind the sequence count as zeros, whatever they hold
   auto load = [&](const float* src, int64_t pitch, float* dst, int dst_pitch, int j0) {
@@ -179,37 +179,48 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     __syncthreads();
     load(v, ld.v, sv, HD, j0);
     if (warp * RPW < n_rows) {
-      float dot[RPW][2] = {};
+      uint64_t dot[RPW][2];  // sums over the even and over the odd columns
+#pragma unroll
+      for (int r = 0; r < RPW; ++r) dot[r][0] = dot[r][1] = 0;
       const float* k0 = sk + lane * L::KP;
       const float* qr = sq + warp * RPW * HD;
 #pragma unroll 2
       for (int c = 0; c < HD; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(k0 + c);
-        const float4 z = *reinterpret_cast<const float4*>(k0 + 32 * L::KP + c);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(k0 + c);
+        const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(k0 + 32 * L::KP + c);
 #pragma unroll
         for (int r = 0; r < RPW; ++r) {
-          const float4 y = *reinterpret_cast<const float4*>(qr + r * HD + c);
-          dot[r][0] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r][0]))));
-          dot[r][1] = fmaf(z.x, y.x, fmaf(z.y, y.y, fmaf(z.z, y.z, fmaf(z.w, y.w, dot[r][1]))));
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(qr + r * HD + c);
+          dot[r][0] = ffma2(x.x, y.x, ffma2(x.y, y.y, dot[r][0]));
+          dot[r][1] = ffma2(z.x, y.x, ffma2(z.y, y.y, dot[r][1]));
         }
       }
 #pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        const float x0 = j0 + lane < lim[r] ? dot[r][0] : -INFINITY;
-        const float x1 = j0 + 32 + lane < lim[r] ? dot[r][1] : -INFINITY;
-        float t = fmaxf(x0, x1);
+      for (int r = 0; r < RPW; r += 2) {
+        float p0[2], p1[2], f[2];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-        const float mn = fmaxf(m[r], t);
-        const float ref = mn == -INFINITY ? 0.0f : mn;  // a row that has seen no key: weights 0
-        const float f = expf(m[r] - ref);
-        const float p0 = expf(x0 - ref), p1 = expf(x1 - ref);
-        m[r] = mn;
-        l[r] = l[r] * f + (p0 + p1);
+        for (int h = 0; h < 2; ++h) {
+          float d0, d1, d2, d3;
+          f32x2_split(dot[r + h][0], d0, d1);
+          f32x2_split(dot[r + h][1], d2, d3);
+          const float x0 = j0 + lane < lim[r + h] ? d0 + d1 : -INFINITY;
+          const float x1 = j0 + 32 + lane < lim[r + h] ? d2 + d3 : -INFINITY;
+          float t = fmaxf(x0, x1);
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[r][c] *= f;
-        sp[r * L::PP + lane] = p0;
-        sp[r * L::PP + 32 + lane] = p1;
+          for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+          const float mn = fmaxf(m[r + h], t);
+          const float ref = mn == -INFINITY ? 0.0f : mn;  // a row that has seen no key: weights 0
+          f[h] = expf(m[r + h] - ref);
+          p0[h] = expf(x0 - ref);
+          p1[h] = expf(x1 - ref);
+          m[r + h] = mn;
+          l[r + h] = l[r + h] * f[h] + (p0[h] + p1[h]);
+        }
+        const uint64_t f2 = f32x2(f[0], f[1]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[r / 2][c] = ffma2(acc[r / 2][c], f2, 0);
+        *reinterpret_cast<float2*>(sp + (r * kKeys + 2 * lane)) = make_float2(p0[0], p0[1]);
+        *reinterpret_cast<float2*>(sp + (r * kKeys + 2 * lane + 64)) = make_float2(p1[0], p1[1]);
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -219,21 +230,28 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     const int n_keys = min(kKeys, seen - j0);
 #pragma unroll 1
     for (int j = 0; j < n_keys; j += 4) {  // (rows behind the sequence are zeros, weights behind `seen` too)
-      float y[4][C];
+      uint64_t y[4][C];  // each value twice
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int c = 0; c < C; c += 2) {
-          const float2 t = *reinterpret_cast<const float2*>(sv + (j + e) * HD + lane * C + c);
-          y[e][c] = t.x;
-          y[e][c + 1] = t.y;
+      for (int e = 0; e < 4; ++e) {
+        const float* at = sv + (j + e) * HD + lane * C;
+        if constexpr (C == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(at);
+          y[e][0] = f32x2(t.x, t.x);
+          y[e][1] = f32x2(t.y, t.y);
+          y[e][2] = f32x2(t.z, t.z);
+          y[e][3] = f32x2(t.w, t.w);
+        } else {
+          const float2 t = *reinterpret_cast<const float2*>(at);
+          y[e][0] = f32x2(t.x, t.x);
+          y[e][1] = f32x2(t.y, t.y);
         }
+      }
 #pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(sp + r * L::PP + j);
+      for (int r = 0; r < RPW; r += 2) {
+        const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(sp + r * kKeys + 2 * j);
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sp + r * kKeys + 2 * j + 4);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          acc[r][c] = fmaf(p.x, y[0][c], fmaf(p.y, y[1][c], fmaf(p.z, y[2][c], fmaf(p.w, y[3][c], acc[r][c]))));
+        for (int c = 0; c < C; ++c) acc[r / 2][c] = ffma2(p.x, y[0][c], ffma2(p.y, y[1][c], ffma2(w.x, y[2][c], ffma2(w.y, y[3][c], acc[r / 2][c]))));
       }
     }
   }
@@ -257,7 +275,12 @@ __global__ void __launch_bounds__(32 * kWarps) packed_f32_kernel(const float* __
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int row = warp * RPW + r;
 #pragma unroll
-    for (int c = 0; c < C; c += 2) *reinterpret_cast<float2*>(sums + row * HD + lane * C + c) = make_float2(acc[r][c], acc[r][c + 1]);
+    for (int c = 0; c < C; c += 2) {
+      float x[2], z[2];
+      f32x2_split(acc[r / 2][c], x[0], x[1]);
+      f32x2_split(acc[r / 2][c + 1], z[0], z[1]);
+      *reinterpret_cast<float2*>(sums + row * HD + lane * C + c) = make_float2(x[r & 1], z[r & 1]);
+    }
     if (lane == 0) *reinterpret_cast<float4*>(sml + row * 4) = make_float4(m[r], sum, 0.0f, 0.0f);
   }
   __syncthreads();
@@ -306,7 +329,7 @@ cudaError_t launch_rows(const PackedArgs& a, int sms, cudaStream_t st) {
   const int64_t n_items = tiles * a.n_kv_heads;
   const Cut cut = choose_cut(a.causal, s, a.n_kv_heads, kKeys, (HD == 64 ? 4 : 2) * sms, kF32Whole, kF32Part, kMaxCluster);
   const F32Items items = {fast_div(a.n_kv_heads), a.n_kv_heads, cut.log_cluster(), static_cast<int32_t>(cut.items), static_cast<int32_t>(n_items)};
-  return launch_items(packed_f32_kernel<HD, RPW, N>, cut, n_items, 32 * kWarps, bytes, st, static_cast<const float*>(a.q),
+  return launch_items(packed_f32_kernel<HD, RPW, N>, cut, n_items, 32 * F32Lay<HD, RPW>::kWarps, bytes, st, static_cast<const float*>(a.q),
                       static_cast<const float*>(a.k), static_cast<const float*>(a.v), static_cast<float*>(a.out), a.lse,
                       Strides{a.ld_q, a.ld_k, a.ld_v, a.ld_out}, s, static_cast<int>(a.n_heads),
                       static_cast<int>(a.n_heads / a.n_kv_heads), a.softmax_scale, static_cast<int>(a.causal), items);
@@ -324,7 +347,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   int64_t blocks = 0;
   for (int i = 0; i < a.n_seqs; ++i)
     blocks += (static_cast<int64_t>(a.q_len[i]) * (a.n_heads / a.n_kv_heads) + 31) / 32 * a.n_kv_heads;
-  return blocks >= sms ? launch_rows<HD, 4, N>(a, sms, st) : launch_rows<HD, 2, N>(a, sms, st);
+  return blocks >= sms ? launch_rows<HD, 8, N>(a, sms, st) : launch_rows<HD, 2, N>(a, sms, st);
 }
 
 cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
