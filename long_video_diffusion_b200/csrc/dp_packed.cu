@@ -5,7 +5,8 @@
 //   out_t,h = sum_j softmax_j(q_t,h . k_j,g * scale) v_j,g,  g = h / group,
 //   j < k_len, causal j <= k_len - q_len + t;  lse_t,h = log sum_j exp(q_t,h . k_j,g * scale)
 //
-// One pass over the keys with a running maximum and sum.
+// One pass over the keys with a running maximum and sum; with few rows the keys are cut over the blocks
+// of a cluster, which join their parts through distributed shared memory in a fixed order.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -109,9 +110,11 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-// A warp's RPW rows against a tile of 64 keys: a lane holds two keys' scores of each row, then,
-// with the weights in shared memory, HD / 32 columns of each row's output.  Either way a 16-byte
-// read from shared memory feeds two to four multiply-adds per lane.
+// A warp's RPW rows against a tile of 64 keys: a lane holds two keys' scores of each row, then, with
+// the weights in shared memory, HD / 32 columns of each row's output.  Bound by the reads from shared
+// memory: at eight rows a 16-byte read feeds 6 (scores) to 11 (outputs) multiply-adds per lane, which go
+// in pairs (even and odd columns of a score, two rows of an output).  2048 causal tokens of 16 heads of
+// 128: 475 us, 36 TFLOP/s (about half of what the multiply-adds alone allow).
 template <int HD, int RPW, int N>
 __global__ void __launch_bounds__(32 * F32Lay<HD, RPW>::kWarps) packed_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                                  const float* __restrict__ v, float* __restrict__ out,
@@ -335,10 +338,12 @@ cudaError_t launch_rows(const PackedArgs& a, int sms, cudaStream_t st) {
                       static_cast<int>(a.n_heads / a.n_kv_heads), a.softmax_scale, static_cast<int>(a.causal), items);
 }
 
-// Four rows per warp, 32 per block; two while those blocks do not even fill the SMs once (single
-// tokens, short prompts).  Measured, us, two | four rows: one head over 512 tokens (16 blocks of 32
-// rows) 46 | 60, 4 of 3000 keys' single tokens (32) 285 | 357, eight k/v heads over 540 tokens (680)
-// 98 | 85, 2048 tokens x 16 heads (1024) 977 | 773.  Eight: 92, 500, 85, 817.
+// 32 rows per block: four warps of eight rows, the fewest reads from shared memory; while such blocks
+// do not fill half the SMs (single tokens, short prompts) eight warps of two, whose blocks of 16 rows
+// are twice as many and each warp's chain shorter.  Measured, us, two | eight rows: one head over 512
+// tokens (16 blocks of 32 rows) 12.7 | 18.8, four single tokens over 100 to 4000 keys, 8 k/v heads
+// (32) 31 | 46, 8 heads on 4 over 512 (128) 23.5 | 20.4, 40 heads on 8 over 540 (680) 80 | 64, 2048
+// tokens x 16 heads (1024) 772 | 475.  Four rows in eight warps: 16.8, 39, 23.7, 69, 533.
 template <int HD, int N>
 cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   int dev = 0, sms = 148;
@@ -347,7 +352,7 @@ cudaError_t launch_n(const PackedArgs& a, cudaStream_t st) {
   int64_t blocks = 0;
   for (int i = 0; i < a.n_seqs; ++i)
     blocks += (static_cast<int64_t>(a.q_len[i]) * (a.n_heads / a.n_kv_heads) + 31) / 32 * a.n_kv_heads;
-  return blocks >= sms ? launch_rows<HD, 8, N>(a, sms, st) : launch_rows<HD, 2, N>(a, sms, st);
+  return 2 * blocks >= sms ? launch_rows<HD, 8, N>(a, sms, st) : launch_rows<HD, 2, N>(a, sms, st);
 }
 
 cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
