@@ -288,10 +288,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tok = p.by_group.div(row);
     const int head = kv * p.group + row - tok * p.group;
     const bool sees = min(k_len, keys_seen(tok, q_len, k_len, p.causal)) > 0;
-    const float inv = sees ? 1.0f / l : 0.0f;
+    const float inv = 1.0f / l;
     const int64_t at = first_q + static_cast<int64_t>(tok);
+    // a row that sees nothing: zeros, not 0 times what the weights of 0 made of hidden values
     *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
-        make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+        sees ? make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv)) : make_uint2(0, 0);
     if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + (log2f(l) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
   };
   for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
