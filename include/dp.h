@@ -519,8 +519,8 @@ dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, cons
  * hold.  A sequence's values have to be finite: one that the causal mask hides takes part in a
  * product with weight 0.  (A key that is hidden may hold anything.)  A query with a score that is
  * NaN or +infinity, or none above -infinity, gets out = NaN.
- * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32)
- * or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
+ * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32;
+ * f16 outputs saturate at +-65504) or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
  * <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative length or start, n_seqs outside
  * [1, DP_MAX_SEQS], sequences that reach behind q_rows or k_rows, and an out or lse whose
  * address range overlaps another tensor's.  No query rows: nothing is done. */

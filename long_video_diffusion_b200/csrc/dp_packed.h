@@ -1,6 +1,7 @@
 // What the packed-attention kernels share: the sequences as a kernel argument, the tiles.
 #pragma once
 
+#include "dp_device.cuh"
 #include "dp_internal.h"
 
 namespace dp {
@@ -47,6 +48,14 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N>& s, int t) {
       hi = mid - 1;
   }
   return lo;
+}
+
+// Two outputs.  The weights that meet the values are rounded, those in the row sum are not, so an
+// output can pass the largest value by half a step of a weight, 2^-11 of it in f16; behind f16's end
+// it saturates (NaN stays NaN).
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+  return F16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi);
 }
 
 // Keys that token `tok` of a sequence sees.

@@ -85,6 +85,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Two softmax weights.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t at = first_q + static_cast<int64_t>(tok);
     // a row that sees nothing: zeros, not 0 times what the weights of 0 made of hidden values
     *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
-        sees ? make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv)) : make_uint2(0, 0);
+        sees ? make_uint2(pack_out<F16>(a.x * inv, a.y * inv), pack_out<F16>(a.z * inv, a.w * inv)) : make_uint2(0, 0);
     if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + (log2f(l) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
   };
   for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {

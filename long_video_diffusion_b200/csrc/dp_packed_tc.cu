@@ -169,6 +169,7 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t a) {
   return v;
 }
 
+// Two softmax weights.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
                 uint32_t x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  x[e] = pack2<F16>(__uint_as_float(r[q * 8 + 2 * e]) * inv_l, __uint_as_float(r[q * 8 + 2 * e + 1]) * inv_l);
+                  x[e] = pack_out<F16>(__uint_as_float(r[q * 8 + 2 * e]) * inv_l, __uint_as_float(r[q * 8 + 2 * e + 1]) * inv_l);
                 *piece(t, h * 4 + q) = sees ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0, 0, 0, 0);
               }
             }
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
       const float inv = sees ? 1.0f / l : 0.0f;
       const int64_t at = first_q + static_cast<int64_t>(tok);
       *reinterpret_cast<uint2*>(p.out + at * p.ld_out + head * HD + c) =
-          make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+          make_uint2(pack_out<F16>(a.x * inv, a.y * inv), pack_out<F16>(a.z * inv, a.w * inv));
       if (p.lse && c == 0) p.lse[at * p.n_heads + head] = sees ? (top + (log2f(l) - kWeightLog2<F16>)) * 0.6931471805599453f : -INFINITY;
     }
     cluster_sync();  // no block leaves while another reads its shared memory

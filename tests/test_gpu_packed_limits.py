@@ -1,9 +1,11 @@
 """GPU parity of packed attention where its promises are tightest: rows that see nothing beside
-keys that hold anything.  Bounds: see test_gpu_packed_attention.py."""
+keys that hold anything, f16 outputs at the type's end.  Bounds: see test_gpu_packed_attention.py."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_packed_attention import BF16, F16, F32, _inputs, _run
+from test_gpu_packed_attention import BF16, F16, F32, _check, _inputs, _run
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -22,3 +24,25 @@ def test_rows_that_see_nothing_are_zeros(dp, q_len, k_len, d, dtype):
         blind = q_len - k_len
         assert not bool(out[:blind].any())
         assert bool(torch.isneginf(lse[:blind]).all())
+
+
+@pytest.mark.parametrize("q_len", [1, 40, 300])
+@pytest.mark.parametrize("k_len", [64, 1024, 6000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_f16_outputs_stay_finite(dp, d, q_len, k_len):
+    """Values at f16's end under weights that all round up: an output is an average of values, so
+    it is no larger than the largest.  Every 16th key has the score 0, the others one whose weight
+    lies 0.5 above a tie (16392 of 32768) and rounds up by 7.5 / 16392.5: 15 of 16 of them move an
+    output by 4.0e-4 of its value, beyond 65520, where f16 ends."""
+    target = math.log(16392.5 / 32768)
+    q = torch.zeros(q_len, 2, d)
+    q[:, :, :2] = 1.0
+    k = torch.zeros(k_len, 1, d)
+    k[:, :, 0] = torch.tensor(target).to(F16).float()                     # and what that leaves, to 2^-22
+    k[:, :, 1] = target - float(torch.tensor(target).to(F16))
+    k[::16] = 0.0
+    q, k = q.to(F16), k.to(F16)
+    for top in (65504.0, -65504.0):
+        v = torch.full((k_len, 1, d), top).to(F16)
+        out, lse = _run(dp, q, k, v, [q_len], [k_len], causal=False, scale=1.0)
+        _check(out, lse, q, k, v, [q_len], [k_len], None, False, scale=1.0)
