@@ -457,7 +457,7 @@ dp_status dp_context_refresh_sublayer(const void* x_ctx, int64_t n_ctx, const dp
 
 /*
  * Microscaled 4-bit floating point (the OCP Microscaling Formats specification v1.0, FP4):
- * a matrix [rows][k], k a multiple of 32, is held as
+ * a matrix [rows][k], k a multiple of 32 and at most 2^31 - 256 (UNSUPPORTED otherwise), is held as
  *   codes   DEVICE [rows][k / 2] bytes: element 2 i of a row in the low half of its byte i,
  *           2 i + 1 in the high half; each the sign and the magnitude 0, 0.5, 1, 1.5, 2, 3,
  *           4 or 6 (e2m1);
@@ -470,7 +470,7 @@ dp_status dp_context_refresh_sublayer(const void* x_ctx, int64_t n_ctx, const dp
 #define DP_MX4_BLOCK 32
 
 /* Bytes of the scales of [rows][k]: ceil(rows / 128) * ceil(k / 128) * 512.  INVALID_ARG for
- * rows < 0, k <= 0 or k no multiple of 32. */
+ * rows outside [0, 2^31), k <= 0, no multiple of 32 or above 2^31 - 256. */
 dp_status dp_mx4_scale_bytes(int64_t rows, int32_t k, int64_t* bytes);
 
 /* Quantise x (DEVICE [n_rows][k], bf16, f16 or f32): for each block of 32, with m its largest

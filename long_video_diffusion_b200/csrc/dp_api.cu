@@ -984,10 +984,13 @@ dp_status dp_sublayer_step(const void* x, int64_t n_win, const dp_blocks* blk, c
 
 namespace {
 
+constexpr int32_t kMx4MostK = INT32_MAX - 255;  // k rounded up to a step of the product stays below 2^31
+
 dp_status check_mx4(int64_t rows, int32_t k) {
   if (rows < 0 || rows > INT32_MAX) return fail(DP_ERR_INVALID_ARG, "rows %lld", static_cast<long long>(rows));
   if (k <= 0) return fail(DP_ERR_INVALID_ARG, "k %d", k);
-  if (k % DP_MX4_BLOCK) return fail(DP_ERR_UNSUPPORTED, "k %d (a multiple of %d)", k, DP_MX4_BLOCK);
+  if (k % DP_MX4_BLOCK || k > kMx4MostK)
+    return fail(DP_ERR_UNSUPPORTED, "k %d (a multiple of %d, at most %d)", k, DP_MX4_BLOCK, kMx4MostK);
   return DP_OK;
 }
 
@@ -997,9 +1000,9 @@ int64_t mx4_scale_size(int64_t rows, int32_t k) { return (rows + 127) / 128 * ((
 
 dp_status dp_mx4_scale_bytes(int64_t rows, int32_t k, int64_t* bytes) {
   if (!bytes) return fail(DP_ERR_INVALID_ARG, "bytes is NULL");
-  if (rows < 0 || rows > INT32_MAX || k <= 0 || k % DP_MX4_BLOCK)
-    return fail(DP_ERR_INVALID_ARG, "rows %lld, k %d (a positive multiple of %d)", static_cast<long long>(rows), k,
-                DP_MX4_BLOCK);
+  if (rows < 0 || rows > INT32_MAX || k <= 0 || k % DP_MX4_BLOCK || k > kMx4MostK)
+    return fail(DP_ERR_INVALID_ARG, "rows %lld, k %d (a positive multiple of %d, at most %d)", static_cast<long long>(rows), k,
+                DP_MX4_BLOCK, kMx4MostK);
   *bytes = mx4_scale_size(rows, k);
   return DP_OK;
 }
