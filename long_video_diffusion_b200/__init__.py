@@ -577,10 +577,15 @@ def _launch(fn, where: str, dev: int, stream, args) -> None:
         raise DpError(st, where)
 
 
+_2_31 = 1 << 31
+
+
 def mx4_scale_bytes(rows: int, k: int) -> int:
     """Bytes of the scales of a [rows][k] matrix in 4 bits (dp_mx4_scale_bytes)."""
+    # ctypes cuts off what 32 or 64 bits do not hold: refused sizes that they do instead
+    rows, k = max(-1, min(int(rows), _2_31)), max(-1, min(int(k), _2_31 - 1))
     out = _I64()
-    _check(_lib.dp_mx4_scale_bytes(int(rows), int(k), ctypes.byref(out)), "dp_mx4_scale_bytes")
+    _check(_lib.dp_mx4_scale_bytes(rows, k, ctypes.byref(out)), "dp_mx4_scale_bytes")
     return out.value
 
 
@@ -601,6 +606,8 @@ def _mx4(codes: torch.Tensor, scales: torch.Tensor):
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("tensor must be contiguous")
     rows, half = codes.shape
+    if rows >= _2_31 or 2 * half >= _2_31:  # ctypes would cut them off
+        raise ValueError(f"[{rows}, {2 * half}] in 4 bits: rows and columns must be below 2^31")
     if scales.numel() < (rows + 127 >> 7) * (half + 63 >> 6) * 512:
         raise ValueError(f"scales hold fewer than mx4_scale_bytes({rows}, {2 * half}) bytes")
     return rows, half
