@@ -53,6 +53,15 @@ __device__ __forceinline__ bool elect_one() {
 // takes tensor memory (which a block of theirs on the same SM may still have to take).
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// 16 bytes that are read once.  What a kernel launched so reads may still be written while its blocks
+// are resident: this load stays behind the wait above, and such kernels use no read-only loads (__ldg,
+// const __restrict__), which hold the data for constant all the while.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // The next kernel's blocks may come as soon as all of this one's have got here (they wait as above).
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

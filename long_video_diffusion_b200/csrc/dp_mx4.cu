@@ -95,9 +95,7 @@ __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restrict__ x, uint32_t* __restrict__ codes,
-                                                                uint32_t* __restrict__ scales, int64_t n_rows, int k,
-                                                                int tiles) {
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint32_t* codes, uint32_t* scales, int64_t n_rows, int k, int tiles) {
   constexpr bool kWide = sizeof(T) == 4;
   let_next_kernel_start();
   wait_for_earlier_kernels();
@@ -113,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restr
   for (int j = 0; j < 4; ++j, src += step)
 #pragma unroll
     for (int h = 0; h < (kWide ? 2 : 1); ++h)
-      raw[j][h] = 32 * j < rows ? __ldcs(reinterpret_cast<const uint4*>(src) + h) : make_uint4(0, 0, 0, 0);
+      raw[j][h] = 32 * j < rows ? ld_once(reinterpret_cast<const uint4*>(src) + h) : make_uint4(0, 0, 0, 0);
   // each row's largest magnitude in its block of 32 (four threads), as fp32 bits
   uint32_t top[4];
   if constexpr (kWide) {
@@ -177,9 +175,7 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* __restr
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
-                                                                  const uint32_t* __restrict__ scales,
-                                                                  T* __restrict__ y, int64_t n_rows, int k, int tiles) {
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* codes, const uint32_t* scales, T* y, int64_t n_rows, int k, int tiles) {
   let_next_kernel_start();
   wait_for_earlier_kernels();
   const Unit u = unit_of_thread(tiles);
@@ -187,11 +183,11 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t
   const int rows = static_cast<int>(min(n_rows - u.row0, static_cast<int64_t>(128)));
   const int64_t at = u.row0 * k + u.col;
   const int64_t step = 32ll * k;
-  const uint4 s4 = __ldg(reinterpret_cast<const uint4*>(scales + (mx4_scale_at(u.row0, u.tile * 4, tiles) >> 2)));
+  const uint4 s4 = *reinterpret_cast<const uint4*>(scales + (mx4_scale_at(u.row0, u.tile * 4, tiles) >> 2));
   const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
   uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = 32 * j < rows ? __ldg(codes + (at >> 3) + j * (step >> 3)) : 0u;
+  for (int j = 0; j < 4; ++j) c[j] = 32 * j < rows ? codes[(at >> 3) + j * (step >> 3)] : 0u;
   T* d = y + at;
 #pragma unroll
   for (int j = 0; j < 4; ++j, d += step) {

@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint16_t* src = p.q + (first_q + static_cast<int64_t>(tok)) * p.ld_q + (kv * p.group + row - tok * p.group) * HD + pair;
 #pragma unroll
       for (int c = 0; c < HD / 16; ++c) {
-        qf[c][h] = row < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16)) : 0u;
-        qf[c][h + 2] = row < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + 8)) : 0u;
+        qf[c][h] = row < rows ? *reinterpret_cast<const uint32_t*>(src + c * 16) : 0u;
+        qf[c][h + 2] = row < rows ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
       }
     }
     float o[HD / 8][4];
