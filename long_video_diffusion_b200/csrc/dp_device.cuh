@@ -63,6 +63,8 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
 }
 
 // The next kernel's blocks may come as soon as all of this one's have got here (they wait as above).
+// Called behind the wait: a kernel that is not ours may read, ahead of its own wait, data that this one does
+// not write, and the kernels ahead of this one would still be at it.
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ mbarrier

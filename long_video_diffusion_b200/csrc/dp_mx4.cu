@@ -97,8 +97,8 @@ __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint32_t* codes, uint32_t* scales, int64_t n_rows, int k, int tiles) {
   constexpr bool kWide = sizeof(T) == 4;
-  let_next_kernel_start();
   wait_for_earlier_kernels();
+  let_next_kernel_start();
   const Unit u = unit_of_thread(tiles);
   const int sub = threadIdx.x & 15;
   // (bound by the issue slots as much as by the memory: one address, one row count, few selects)
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* codes, const uint32_t* scales, T* y, int64_t n_rows, int k, int tiles) {
-  let_next_kernel_start();
   wait_for_earlier_kernels();
+  let_next_kernel_start();
   const Unit u = unit_of_thread(tiles);
   if (u.row0 >= n_rows || u.col >= k) return;
   const int rows = static_cast<int>(min(n_rows - u.row0, static_cast<int64_t>(128)));

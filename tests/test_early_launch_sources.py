@@ -34,3 +34,12 @@ def test_no_global_data_is_taken_for_constant(name):
 def test_every_kernel_waits_for_the_ones_ahead(name):
     kernels = re.split(r"__global__", _code(name))[1:]
     assert kernels and all("wait_for_earlier_kernels();" in k for k in kernels)
+
+
+@pytest.mark.parametrize("name", EARLY)
+def test_the_next_kernel_starts_behind_the_wait(name):
+    """A kernel behind may read, before a wait of its own, what its predecessor does not write: it
+    must not start while kernels ahead of this one still run."""
+    for kernel in re.split(r"__global__", _code(name))[1:]:
+        at = kernel.find("let_next_kernel_start();")
+        assert at < 0 or 0 <= kernel.find("wait_for_earlier_kernels();") < at
