@@ -56,7 +56,7 @@ constexpr float kRescaleLog2 = 8.0f;
 
 // 2^x on the FMA pipe for some columns (the MUFU unit gives 16 exponentials per clock and SM, as
 // many as the tensor cores need at head_dim 128): n = round(x), 2^n p(x - n), p the degree-4
-// minimax polynomial of 2^f on [-1/2, 1/2] (csrc/fit_exp2_poly.py with DEGREE = 4; relative error
+// minimax polynomial of 2^f on [-1/2, 1/2] (csrc/fit_exp2_poly.py 4; relative error
 // 2.7e-6, so that the row sum and the log-sum-exp keep fp32's use).
 constexpr float kC0 = 0.9999992847442627f, kC1 = 0.6931217908859253f, kC2 = 0.240247443318367f;
 constexpr float kC3 = 0.05591785907745361f, kC4 = 0.009570102207362652f;
@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(Lay<HD>::kThreads, 1)
         f32x2_split(fadd2(acc0, acc1), a0, a1);
         l_sum += a0 + a1;
         // A NaN score (or infinity - infinity) is a weight of NaN, or 3.4e38 by the polynomial's integer
-        // addition; true sums stay below 2^8 times 2^31 keys.  From here on the row is NaN.
+        // addition; true weights stay below 2^8 (in f16 2^15), true sums below 2^31 of them.  From here on
+        // the row is NaN.
         if (!(l_sum < kLost)) l_sum = NAN;
         tmem_wait_st();
         tc_fence_before();
