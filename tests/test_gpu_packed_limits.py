@@ -1,5 +1,6 @@
 """GPU parity of packed attention where its promises are tightest: rows that see nothing beside
-keys that hold anything, f16 outputs at the type's end.  Bounds: see test_gpu_packed_attention.py."""
+keys that hold anything, f16 outputs at the type's end, head
+groups whose cuts differ in size.  Bounds: see test_gpu_packed_attention.py."""
 import math
 
 import pytest
@@ -46,3 +47,16 @@ def test_f16_outputs_stay_finite(dp, d, q_len, k_len):
         v = torch.full((k_len, 1, d), top).to(F16)
         out, lse = _run(dp, q, k, v, [q_len], [k_len], causal=False, scale=1.0)
         _check(out, lse, q, k, v, [q_len], [k_len], None, False, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("heads,kv_heads", [(129, 1), (258, 2), (387, 3)])
+@pytest.mark.parametrize("q_lens,k_lens", [([70, 33, 1], [70, 33, 1]), ([2, 1], [5000, 300]), ([1], [9000])],
+                         ids=lambda x: "_".join(map(str, x)))
+def test_head_groups_cut_unevenly(dp, q_lens, k_lens, heads, kv_heads, dtype):
+    """Groups of 129 heads are cut into 65 and 64: the second cut's tile reaches into the next
+    k/v head's query heads, or behind the last; with many keys these are cut too."""
+    for d in (64, 128):
+        q, k, v = _inputs(q_lens, k_lens, heads, kv_heads, d, dtype)
+        out, lse = _run(dp, q, k, v, q_lens, k_lens)
+        _check(out, lse, q, k, v, q_lens, k_lens, None, True)
