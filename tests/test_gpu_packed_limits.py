@@ -1,8 +1,10 @@
 """GPU parity of packed attention where its promises are tightest: rows that see nothing beside
 keys that hold anything, f16 outputs at the type's end, head
-groups whose cuts differ in size.  Bounds: see test_gpu_packed_attention.py."""
+groups whose cuts differ in size, single tokens beside prompts on both sides of the rule that gives
+them a launch of their own.  Bounds: see test_gpu_packed_attention.py."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -60,3 +62,28 @@ def test_head_groups_cut_unevenly(dp, q_lens, k_lens, heads, kv_heads, dtype):
         q, k, v = _inputs(q_lens, k_lens, heads, kv_heads, d, dtype)
         out, lse = _run(dp, q, k, v, q_lens, k_lens)
         _check(out, lse, q, k, v, q_lens, k_lens, None, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,d", [(16, 16, 64), (8, 4, 64), (8, 4, 128), (8, 8, 128)])
+def test_tokens_beside_prompts_in_one_launch_and_in_two(dp, heads, kv_heads, d, apart, dtype):
+    """Sequences of at most 16 rows under a k/v head get a launch of their own from 40 tiles of 64
+    keys per SM on: a fifth below that and a fifth above, so that neither side is missed."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(heads + d)
+    goal = 40 * sms * (1.2 if apart else 0.8) / kv_heads             # tiles of all tokens under one k/v head
+    k_lens, q_lens = [], []
+    while goal > 0:
+        n = int(min(rng.integers(500, 4000), 64 * goal + 1))
+        k_lens.append(n)
+        q_lens.append(int(rng.integers(1, 1 + 16 * kv_heads // heads)))
+        goal -= (n + 63) // 64
+    tiles = sum((n + 63) // 64 for n in k_lens) * kv_heads
+    assert (tiles >= 44 * sms) if apart else (tiles <= 36 * sms)
+    for at, ql, kl in ((0, 140, 300), (1, 0, 70), (len(q_lens), 65, 65), (len(q_lens), 20, 5)):
+        q_lens.insert(at, ql)
+        k_lens.insert(at, kl)
+    q, k, v = _inputs(q_lens, k_lens, heads, kv_heads, d, dtype)
+    out, lse = _run(dp, q, k, v, q_lens, k_lens)
+    _check(out, lse, q, k, v, q_lens, k_lens, None, True)
