@@ -483,13 +483,14 @@ dp_status dp_mx4_quantize(const void* x, int64_t n_rows, int32_t k, dp_dtype x_d
                           void* stream);
 
 /* The values that codes and scales stand for: y DEVICE [n_rows][k], bf16 or f32 (exact; what
- * underflows in y's type is rounded) or f16 (rounded to nearest even, saturating at +-65504). */
+ * underflows in y's type is rounded, what passes fp32's end, at scales of 253 and 254, is infinite) or f16 (rounded to nearest even, saturating at +-65504). */
 dp_status dp_mx4_dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y, dp_dtype y_dt,
                             void* stream);
 
 /* y = a W^T + bias with both operands in 4 bits: a [m][k] and w [n][k] as codes and scales
  * (w's rows are the out-features), bias DEVICE [n] float or NULL, y DEVICE [m][n] of y_dt
- * (bf16, f16 saturating at +-65504, or f32).  The products are exact, their sums fp32, rounded
+ * (bf16, f16 saturating at +-65504, or f32).  A product of two elements is exact in fp32's normal
+ * range [2^-126, 2^128), infinite above, off by less than 2^-126 below; the sums are fp32, rounded
  * once to y's type.  n a multiple of 8, k of 32 (UNSUPPORTED otherwise).  m = 0 does nothing.
  * y overlaps no input. */
 dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, const void* w_scales, const float* bias,
