@@ -483,7 +483,8 @@ dp_status dp_mx4_quantize(const void* x, int64_t n_rows, int32_t k, dp_dtype x_d
                           void* stream);
 
 /* The values that codes and scales stand for: y DEVICE [n_rows][k], bf16 or f32 (exact; what
- * underflows in y's type is rounded, what passes fp32's end, at scales of 253 and 254, is infinite) or f16 (rounded to nearest even, saturating at +-65504). */
+ * underflows in y's type is rounded, what passes fp32's end, at scales of 253 and 254, is infinite)
+ * or f16 (rounded to nearest even, saturating at +-65504). */
 dp_status dp_mx4_dequantize(const void* codes, const void* scales, int64_t n_rows, int32_t k, void* y, dp_dtype y_dt,
                             void* stream);
 
@@ -518,8 +519,10 @@ dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, cons
  * of 16 bytes, at most 2^28 elements); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
  * sequence are neither read nor written, key rows of no sequence affect nothing, whatever they
  * hold.  A sequence's values have to be finite: one that the causal mask hides takes part in a
- * product with weight 0.  (A key that is hidden may hold anything.)  A query with a score that is
- * NaN or +infinity, or none above -infinity, gets out = NaN.
+ * product with weight 0.  (A key that is hidden may hold anything.)  In bf16 and f32 they stay below
+ * 2^120 / k_lens[i]: the fp32 sums of weights, up to 2^8 each, times values have to as well (f16
+ * values always do).  A query with a score that is NaN or +infinity, or none above -infinity, gets
+ * out = NaN.
  * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32;
  * f16 outputs saturate at +-65504) or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
  * <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative length or start, n_seqs outside

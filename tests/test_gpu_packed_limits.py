@@ -1,7 +1,7 @@
 """GPU parity of packed attention where its promises are tightest: rows that see nothing beside
-keys that hold anything, f16 outputs at the type's end, head
-groups whose cuts differ in size, single tokens beside prompts on both sides of the rule that gives
-them a launch of their own.  Bounds: see test_gpu_packed_attention.py."""
+keys that hold anything, outputs and values at the types' ends, head groups whose cuts differ in
+size, single tokens beside prompts on both sides of the rule that gives them a launch of their own.
+Bounds: see test_gpu_packed_attention.py."""
 import math
 
 import numpy as np
@@ -87,3 +87,21 @@ def test_tokens_beside_prompts_in_one_launch_and_in_two(dp, heads, kv_heads, d, 
     q, k, v = _inputs(q_lens, k_lens, heads, kv_heads, d, dtype)
     out, lse = _run(dp, q, k, v, q_lens, k_lens)
     _check(out, lse, q, k, v, q_lens, k_lens, None, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("q_len", [1, 40, 300])
+@pytest.mark.parametrize("grow", [0.0, 5.0])
+def test_values_up_to_the_stated_size(dp, q_len, grow, dtype):
+    """Values of up to 2^120 over the number of keys: with equal scores, and with scores that grow by
+    up to 5 (7.2 in log2, less than what the running maximum may lag) along the keys."""
+    n = 1000
+    for d in (64, 128):
+        q, k, v = _inputs([q_len], [n], 2, 1, d, dtype, spare=0)
+        q[:], k[:] = 0.0, 0.0
+        q[:, :, 0] = 1.0
+        k[:, :, 0] = (torch.linspace(0.0, grow, n)[:, None]).to(dtype)
+        v = (torch.sign(v.float()) * 2.0 ** 120 / n).to(dtype)
+        v[:, :, ::2] = v[:, :, ::2].abs()
+        out, lse = _run(dp, q, k, v, [q_len], [n], causal=False, scale=1.0)
+        _check(out, lse, q, k, v, [q_len], [n], None, False, scale=1.0)
