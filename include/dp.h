@@ -505,29 +505,31 @@ dp_status dp_mx4_linear(const void* a, const void* a_scales, const void* w, cons
 #define DP_CAUSAL 1u
 
 /* Attention over n_seqs sequences packed one behind the other (q_lens, k_lens, k_starts: HOST
- * arrays).  Sequence i owns q_lens[i] query rows (behind those of the sequences before it) and
- * the key rows [k_starts[i], k_starts[i] + k_lens[i]); k_starts = NULL: one behind the other
- * like the queries.  Key ranges may overlap (a shared prefix) and leave rows out (a padded
- * cache).  Its queries are the sequence's last rows: with DP_CAUSAL query t sees the keys
- * j <= k_lens[i] - q_lens[i] + t, without it all k_lens[i].
+ * arrays, read during the call: one captured into a graph keeps the lengths of its capture).
+ * Sequence i owns q_lens[i] query rows (behind those of the sequences before it) and the key rows
+ * [k_starts[i], k_starts[i] + k_lens[i]); k_starts = NULL: one behind the other like the queries.
+ * Key ranges may overlap (a shared prefix) and leave rows out (a padded cache).  Its queries are
+ * the sequence's last rows: with DP_CAUSAL query t sees the keys j <= k_lens[i] - q_lens[i] + t,
+ * without it all k_lens[i].
  *   out_t,h = sum_j softmax_j(q_t,h . k_j,g * softmax_scale) v_j,g,   g = h / (n_heads / n_kv_heads)
  *   lse_t,h = log sum_j exp(q_t,h . k_j,g * softmax_scale)
  * A query that sees no key (k_lens[i] = 0, or causal with more queries than keys) gets out = 0
  * and lse = -infinity.
  * q, out: DEVICE [q_rows][n_heads][head_dim], k, v: DEVICE [k_rows][n_kv_heads][head_dim], all
  * of dt, rows ld_* elements apart (so that they may be column ranges of one buffer; multiples
- * of 16 bytes, at most 2^28 elements); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows behind the last
- * sequence are neither read nor written, key rows of no sequence affect nothing, whatever they
- * hold.  A sequence's values have to be finite: one that the causal mask hides takes part in a
- * product with weight 0.  (A key that is hidden may hold anything.)  In bf16 and f32 they stay below
- * 2^120 / k_lens[i]: the fp32 sums of weights, up to 2^8 each, times values have to as well (f16
- * values always do).  A query with a score that is NaN or +infinity, or none above -infinity, gets
- * out = NaN.
- * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32;
- * f16 outputs saturate at +-65504) or f32 (all in fp32).  head_dim 64 or 128; n_heads a multiple of n_kv_heads.  softmax_scale
- * <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative length or start, n_seqs outside
- * [1, DP_MAX_SEQS], sequences that reach behind q_rows or k_rows, and an out or lse whose
- * address range overlaps another tensor's.  No query rows: nothing is done. */
+ * of 16 bytes, at most 2^28 elements); lse: DEVICE [q_rows][n_heads] float or NULL.  Query rows
+ * behind the last sequence are neither read nor written, key rows of no sequence affect nothing,
+ * whatever they hold.  A sequence's values have to be finite: one that the causal mask hides takes
+ * part in a product with weight 0.  (A key that is hidden may hold anything.)  In bf16 and f32
+ * values stay below 2^120 / k_lens[i]: fp32 holds the sums of weights, up to 2^8 each, times values
+ * (of f16 values always).  A query with a score that is NaN or +infinity, or none above -infinity,
+ * gets out = NaN.
+ * dt: bf16 or f16 (tensor cores; the softmax weights rounded to dt, sums and statistics fp32; f16
+ * outputs saturate at +-65504) or f32 (all in fp32).  head_dim 64 or 128; n_heads at most 32767, a
+ * multiple of n_kv_heads.  softmax_scale <= 0 selects 1/sqrt(head_dim).  INVALID_ARG for a negative
+ * length or start, n_seqs outside [1, DP_MAX_SEQS], sequences that reach behind q_rows or k_rows,
+ * and an out or lse whose address range overlaps another tensor's.  No query rows: nothing is
+ * done. */
 dp_status dp_packed_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
                               void* out, int64_t ld_out, float* lse, int64_t q_rows, int64_t k_rows,
                               const int64_t* q_lens, const int64_t* k_lens, const int64_t* k_starts, int32_t n_seqs,

@@ -680,7 +680,9 @@ def packed_attention(q, k, v, q_lens: Sequence[int], k_lens: Sequence[int], out,
     behind the other, and the key rows [k_starts[i], k_starts[i] + k_lens[i]) (k_starts=None: one
     behind the other too).  Its queries are its last rows: causal, query t sees the keys
     j <= k_lens[i] - q_lens[i] + t.  lse: float32 [q_rows, heads] or None.  A query that sees no
-    key gets out = 0 and lse = -inf; rows behind the last sequence are left as they are."""
+    key gets out = 0 and lse = -inf; rows behind the last sequence are left as they are.  A call
+    captured into a graph keeps its lengths and starts: the rows' contents may change between
+    replays, a cache that has grown needs a call of its own."""
     n = len(q_lens)
     if len(k_lens) != n or (k_starts is not None and len(k_starts) != n):
         raise ValueError("q_lens, k_lens and k_starts differ in length")

@@ -105,3 +105,23 @@ def test_values_up_to_the_stated_size(dp, q_len, grow, dtype):
         v[:, :, ::2] = v[:, :, ::2].abs()
         out, lse = _run(dp, q, k, v, [q_len], [n], causal=False, scale=1.0)
         _check(out, lse, q, k, v, [q_len], [n], None, False, scale=1.0)
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_a_captured_call_keeps_its_lengths(dp, q_len):
+    """A replay answers for the lengths of the capture, on what the rows hold at the replay."""
+    q, k, v = (t.cuda() for t in _inputs([q_len], [900], 4, 2, 64, BF16, spare=0))
+    out, want = torch.zeros_like(q), torch.zeros_like(q)
+    q_lens, k_lens, starts = [q_len], [500], [100]
+    dp.packed_attention(q, k, v, q_lens, k_lens, out, k_starts=starts)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dp.packed_attention(q, k, v, q_lens, k_lens, out, k_starts=starts)
+    q_lens[0], k_lens[0], starts[0] = 0, 800, 0
+    k.mul_(-0.5)
+    out.zero_()
+    graph.replay()
+    dp.packed_attention(q, k, v, [q_len], [500], want, k_starts=[100])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and bool(out.any())
