@@ -14,12 +14,14 @@
 // fixed order.  One row by W of 4096 x 4096 (8.9 MB): 4.9 us, where reading W alone takes 1.4 us: the
 // launch, the first bytes' way from memory and the join are the rest.
 //
-// Many rows (mx4_wide_kernel): bound by the tensor cores.  A persistent kernel of block pairs,
+// Many rows (mx4_wide_kernel).  A persistent kernel of block pairs,
 // each pair one output tile of 256 x 256 (tcgen05 cta_group::2: a block holds 128 rows of a and
 // 128 of W, and its half of the sums): at 4 bits a product of 64 of k takes 128 clocks and 8 KB
 // of a block's shared memory, half of what it can read and be filled with in that time, where a
-// block by itself would need 12 KB.  8192 x 8192 x 8192: 207 us, 5.3 PFLOP/s (3.2 times the measured
-// bf16 rate); beyond some 200 us the power limit lowers the clock.
+// block by itself would need 12 KB.  The tensor pipe is busy 62 % of the time; whether the fill from L2
+// (35840 bytes per 512 clocks and block) or the six scale copies ahead of a step's products hold the rest
+// is not told apart.  8192 x 8192 x 8192: 202 us, 5.4 PFLOP/s (3.3 times the measured bf16 rate), and 231
+// in a loop, where the power limit lowers the clock to 1440 of 1965 MHz.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
