@@ -95,7 +95,8 @@ __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint32_t* codes, uint32_t* scales, int64_t n_rows, int k, int tiles) {
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint32_t* codes, uint32_t* scales,
+                                                                int64_t n_rows, int k, int tiles) {
   constexpr bool kWide = sizeof(T) == 4;
   wait_for_earlier_kernels();
   let_next_kernel_start();
@@ -175,7 +176,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* x, uint
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* codes, const uint32_t* scales, T* y, int64_t n_rows, int k, int tiles) {
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* codes, const uint32_t* scales, T* y,
+                                                                  int64_t n_rows, int k, int tiles) {
   wait_for_earlier_kernels();
   let_next_kernel_start();
   const Unit u = unit_of_thread(tiles);

@@ -116,7 +116,8 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
 // in pairs (even and odd columns of a score, two rows of an output).  2048 causal tokens of 16 heads of
 // 128: 475 us, 36 TFLOP/s (about half of what the multiply-adds alone allow).
 template <int HD, int RPW, int N>
-__global__ void __launch_bounds__(32 * F32Lay<HD, RPW>::kWarps) packed_f32_kernel(const float* q, const float* k, const float* v, float* out, float* lse, Strides ld,
+__global__ void __launch_bounds__(32 * F32Lay<HD, RPW>::kWarps) packed_f32_kernel(const float* q, const float* k,
+                                                                 const float* v, float* out, float* lse, Strides ld,
                                                                  const __grid_constant__ PackedSeqs<N> seqs, int n_heads,
                                                                  int group, float scale, int causal, F32Items items) {
   using L = F32Lay<HD, RPW>;

@@ -36,8 +36,8 @@
 // pipe 49 % of the active cycles of 4096 causal tokens, 74 % on the busiest SM; issue slots 43 %): a query
 // tile's softmax and products wait for each other, and two tiles do not quite cover it; long runs meet the
 // power limit besides.  Causal 16384 tokens of 16 heads on 4: head_dim 128 930 to 970 us in short bursts
-// (1.18 PFLOP/s), 1075 in a loop, at 1640 of 1965 MHz; head_dim 64 715, and 755 at 1865 MHz; nine prompts of 1 to 2048 tokens,
-// 32 heads on 8 of 128: 111 us, 123 in a loop at 1770 MHz.
+// (1.18 PFLOP/s), 1075 in a loop, at 1640 of 1965 MHz; head_dim 64 715, and 755 at 1865 MHz; nine prompts
+// of 1 to 2048 tokens, 32 heads on 8 of 128: 111 us, 124 in a loop at 1765 MHz.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -4,8 +4,9 @@ The softmax of the tensor-core attention evaluates exp2 on the MUFU unit (16 res
 clock per SM), which caps head_dim 64 at about half the tensor-core rate.  Part of the
 exponentials therefore run on the FMA pipe instead: x = n + f with n = round(x) and
 f in [-1/2, 1/2]; 2^x = 2^n * p(f), where p is the polynomial of a degree (3 for the window
-attention, 4 for the packed one, whose log-sum-exp is an output) that minimises the maximum relative error |p(f) / 2^f - 1| on [-1/2, 1/2] (Remez exchange, Chebyshev
-alternation: the error equioscillates at degree + 2 points), and 2^n is added to the
+attention, 4 for the packed one, whose log-sum-exp is an output) that minimises the maximum
+relative error |p(f) / 2^f - 1| on [-1/2, 1/2] (Remez exchange, Chebyshev alternation: the error
+equioscillates at degree + 2 points), and 2^n is added to the
 exponent bits of p(f).
 
 Run: python long_video_diffusion_b200/csrc/fit_exp2_poly.py [degree]  -> prints the coefficients
